@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -24,6 +25,13 @@ OUT_F32 = 1
 O_IN_F32 = 2
 PRECISE = 4
 FP16 = 8
+# option bits of forge_qkv_fwd / forge_qkv_bwd
+QKV_ADJACENT = 16
+QKV_GRAD_F32 = 32
+# element types of forge_grad_tensor
+GRAD_F32 = 0
+GRAD_BF16 = 1
+GRAD_F16 = 2
 
 PROBE_SS_KK = 0
 PROBE_SS_KMN = 1
@@ -38,9 +46,13 @@ EXPORTED = [
     "forge_attn_bwd_noalloc", "forge_adamw_workspace_size", "forge_adamw_step",
     "forge_linear_fwd", "forge_linear_bwd_dx", "forge_linear_bwd_dw", "forge_linear_split_k",
     "forge_attn_bf16_to_fp16",
+    "forge_qkv_fwd", "forge_qkv_bwd", "forge_qkv_bwd_workspace_size",
+    "forge_linear_grouped_fwd", "forge_linear_grouped_bwd_dx", "forge_linear_grouped_bwd_dw",
+    "forge_grad_workspace_size", "forge_grad_norm", "forge_grad_clip",
 ]
 
 ADAMW_MAX_TENSORS_PER_LAUNCH = 256
+LINEAR_MAX_EXPERTS = 1024
 
 
 class AdamWTensor(ctypes.Structure):
@@ -49,6 +61,24 @@ class AdamWTensor(ctypes.Structure):
                 ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("n", ctypes.c_longlong), ("decay", ctypes.c_int)]
 
+
+class QkvConfig(ctypes.Structure):
+    """forge_qkv_config of include/forge_attn.h (sizes and device pointers)."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("rot", ctypes.c_int),
+                ("axes", ctypes.c_int), ("eps", ctypes.c_float), ("inv_freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class QkvTensor(ctypes.Structure):
+    """forge_qkv_tensor of include/forge_attn.h (device pointer and strides in elements)."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
+
+
+# forge_grad_tensor of include/forge_adamw.h: grad, out, n, dtype (padded to 8 bytes)
+_GRAD_TENSOR = "QQqi4x"
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -81,6 +111,16 @@ _SIGNATURES = {
     "forge_linear_bwd_dw": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "forge_linear_split_k": (_i, [_i, _i, _i]),
     "forge_attn_bf16_to_fp16": (_i, [_vp, _vp, ctypes.c_longlong, _vp, _vp]),
+    "forge_qkv_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]),
+    "forge_qkv_bwd_workspace_size": (_sz, [_i]),
+    "forge_qkv_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _i,
+                           _vp]),
+    "forge_linear_grouped_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "forge_linear_grouped_bwd_dx": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "forge_linear_grouped_bwd_dw": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "forge_grad_workspace_size": (_sz, [_i]),
+    "forge_grad_norm": (_i, [ctypes.c_char_p, _i, _vp, _vp, _sz, _vp]),
+    "forge_grad_clip": (_i, [ctypes.c_char_p, _i, _f, _vp, _vp, _sz, _vp]),
     "forge_adamw_step": (_i, [ctypes.POINTER(AdamWTensor), _i, _f, _f, _f, _f, _f, _i, _f, _vp,
                               _vp, _sz, _vp]),
 }
@@ -220,6 +260,67 @@ def forge_linear_split_k(tokens, in_features, out_features):
 
 def forge_attn_bf16_to_fp16(src, dst, n, overflow, stream):
     return load().forge_attn_bf16_to_fp16(src, dst, n, overflow, stream)
+
+
+def _ref(value):
+    """Address of a structure (None stays None); the caller keeps the structure alive."""
+    return None if value is None else ctypes.addressof(value)
+
+
+def forge_qkv_fwd(config, q, k, v, q_out, k_out, v_out, flags, stream):
+    """config: a QkvConfig; q, k, v: QkvTensor or None; outputs: device addresses or None."""
+    return load().forge_qkv_fwd(_ref(config), _ref(q), _ref(k), _ref(v), q_out, k_out, v_out, flags,
+                                stream)
+
+
+def forge_qkv_bwd_workspace_size(d):
+    return load().forge_qkv_bwd_workspace_size(d)
+
+
+def forge_qkv_bwd(config, dq, dk, dv, q, k, q_grad, k_grad, v_grad, dq_weight, dk_weight, accumulate,
+                  workspace, workspace_bytes, flags, stream):
+    """config: a QkvConfig; q, k and the *_grad: QkvTensor or None; the rest device addresses."""
+    return load().forge_qkv_bwd(_ref(config), dq, dk, dv, _ref(q), _ref(k), _ref(q_grad),
+                                _ref(k_grad), _ref(v_grad), dq_weight, dk_weight, accumulate,
+                                workspace, workspace_bytes, flags, stream)
+
+
+def forge_linear_grouped_fwd(x, w, y, offsets, rows, experts, in_features, out_features, flags,
+                             stream):
+    return load().forge_linear_grouped_fwd(x, w, y, offsets, rows, experts, in_features,
+                                           out_features, flags, stream)
+
+
+def forge_linear_grouped_bwd_dx(dy, w, dx, offsets, rows, experts, in_features, out_features, flags,
+                                stream):
+    return load().forge_linear_grouped_bwd_dx(dy, w, dx, offsets, rows, experts, in_features,
+                                              out_features, flags, stream)
+
+
+def forge_linear_grouped_bwd_dw(dy, x, dw, offsets, rows, experts, in_features, out_features,
+                                accumulate, flags, stream):
+    return load().forge_linear_grouped_bwd_dw(dy, x, dw, offsets, rows, experts, in_features,
+                                              out_features, accumulate, flags, stream)
+
+
+def forge_grad_workspace_size(n_tensors):
+    return load().forge_grad_workspace_size(n_tensors)
+
+
+def grad_table(fields, n_tensors):
+    """The forge_grad_tensor array of a flat list grad, out, n, dtype, grad, out, ..."""
+    return struct.pack(_GRAD_TENSOR * n_tensors, *fields)
+
+
+def forge_grad_norm(table, n_tensors, norm_out, workspace, workspace_bytes, stream):
+    """table: grad_table() of the tensors."""
+    return load().forge_grad_norm(table, n_tensors, norm_out, workspace, workspace_bytes, stream)
+
+
+def forge_grad_clip(table, n_tensors, max_norm, norm_out, workspace, workspace_bytes, stream):
+    """table: grad_table() of the tensors."""
+    return load().forge_grad_clip(table, n_tensors, max_norm, norm_out, workspace, workspace_bytes,
+                                  stream)
 
 
 def forge_attn_check_device_error(stream):

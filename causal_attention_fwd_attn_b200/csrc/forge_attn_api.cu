@@ -22,6 +22,7 @@ cudaError_t read_and_clear_device_error(unsigned int* value, cudaStream_t stream
     if ((e = read_and_clear_device_error_bwd(&v)) != cudaSuccess) return e;
     if ((e = read_and_clear_device_error_probe(&v)) != cudaSuccess) return e;
     if ((e = read_and_clear_device_error_gemm(&v)) != cudaSuccess) return e;
+    if ((e = read_and_clear_device_error_grouped(&v)) != cudaSuccess) return e;
     *value = v;
     return cudaSuccess;
 }
@@ -95,6 +96,24 @@ cudaError_t encode_map_2d16(CUtensorMap* map, const void* base, long long inner,
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_map_3d(CUtensorMap* map, const void* base, long long inner, long long rows,
+                          long long planes, int box_inner, int box_rows, MapType type) {
+    auto fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const long long el = type == kMapF32 ? 4 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)(inner * el), (cuuint64_t)(inner * rows * el)};
+    cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType dt = type == kMapF32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;

@@ -68,6 +68,46 @@ int forge_adamw_step(const forge_adamw_tensor* tensors, int n_tensors, float lr,
                      float* grad_norm_out, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/*
+ * The global norm of many gradients, and their clipping at it, apart from the step: for
+ * gradients that something else than forge_adamw_step reads, and for 16-bit ones.
+ *
+ *   norm = sqrt(sum over every tensor and element of grad^2)
+ *   c    = max_norm / norm if norm > max_norm, else 1;   out = c * grad
+ *
+ * The sum is held in fp32 within a thread's few values and in fp64 beyond, and does not
+ * overflow or vanish where the norm itself does not.  A NaN among the gradients makes the norm
+ * NaN and leaves c = 1; an infinity makes c = 0 (as in forge_adamw_step): callers that want
+ * to skip such a step read the norm.  Tensors: fp32, bf16 or fp16, mixed, 16-byte aligned, n
+ * contiguous values each; n = 0 is allowed (its pointers may be NULL).  out may be grad (in
+ * place); otherwise outputs must not overlap inputs, and no two tensors may overlap.
+ * Deterministic (no atomics); the workspace's contents on entry do not matter.
+ */
+#define FORGE_GRAD_F32 0
+#define FORGE_GRAD_BF16 1
+#define FORGE_GRAD_F16 2
+
+typedef struct {
+    const void* grad; /* read                                                   */
+    void* out;        /* written by forge_grad_clip, in grad's type             */
+    long long n;      /* values, >= 0                                           */
+    int dtype;        /* FORGE_GRAD_F32, FORGE_GRAD_BF16 or FORGE_GRAD_F16       */
+} forge_grad_tensor;
+
+/* Bytes of device workspace the two calls need for n_tensors tensors (0 if n_tensors < 1). */
+size_t forge_grad_workspace_size(int n_tensors);
+
+/* The norm into the DEVICE float norm_out.  tensors: a HOST array (read during the call
+ * only; out is ignored).  workspace: forge_grad_workspace_size() bytes, 16-byte aligned. */
+int forge_grad_norm(const forge_grad_tensor* tensors, int n_tensors, float* norm_out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm (into norm_out unless that is NULL) and the clipped gradients.  max_norm > 0.  Two
+ * launches per FORGE_ADAMW_MAX_TENSORS_PER_LAUNCH tensors; in place, with nothing to clip,
+ * nothing is written. */
+int forge_grad_clip(const forge_grad_tensor* tensors, int n_tensors, float max_norm,
+                    float* norm_out, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

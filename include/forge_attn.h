@@ -216,6 +216,86 @@ int forge_attn_bwd_noalloc(const void* q, const void* k, const void* v, const vo
 int forge_attn_bf16_to_fp16(const void* src, void* dst, long long n, unsigned int* overflow,
                             void* stream);
 
+/*
+ * The stage between the QKV projection and the attention, in one pass each way: an RMS
+ * norm of every query and key head, rotary positions with one or several axes, and the
+ * change of layout from the projection's token-major rows to the attention's
+ * [B][H][T][d].  (The paper's model adds learned positions to its embeddings and has no
+ * counterpart; models with rotary positions need this stage around its attention.)
+ *
+ *   r = 1 / sqrt(mean_i x_i^2 + eps),  n = r x o weight          (weight NULL: n = x)
+ *   pair j of the first `rot` elements, (a, b):  phi = positions[axis_j][b][t] * inv_freq[j],
+ *     (a, b) -> (a cos phi - b sin phi, a sin phi + b cos phi);  the rest stays as it is.
+ *     Pair j is (j, j + rot / 2), or (2j, 2j + 1) with FORGE_QKV_ADJACENT.
+ *   v is moved only.  H is a multiple of Hkv: key / value head g of the projection becomes
+ *   the attention's heads [g H / Hkv, (g + 1) H / Hkv).
+ *
+ * Angles are reduced in 64 bits, so that positions up to 2^31 keep their phase; all other
+ * arithmetic is in fp32 and each output is rounded once.
+ */
+#define FORGE_QKV_ADJACENT 16 /* pairs of neighbours instead of halves                       */
+#define FORGE_QKV_GRAD_F32 32 /* backward: dq, dk, dv are fp32 (FORGE_ATTN_OUT_F32 outputs of */
+                              /* the attention's backward)                                   */
+
+typedef struct {
+    int B, T;                /* sequences and their tokens                                   */
+    int H, Hkv;              /* the attention's heads; heads of k and v in the projection    */
+    int d;                   /* 64 or 128                                                    */
+    int rot;                 /* rotated elements of a head, 0 (none) to d; even, and a       */
+                             /* multiple of 16 unless FORGE_QKV_ADJACENT                     */
+    int axes;                /* position axes (>= 1)                                         */
+    float eps;               /* >= 0, added to the mean square                               */
+    const double* inv_freq;  /* DEVICE [rot / 2]: angle per position of each pair            */
+    const int* positions;    /* DEVICE [axes][B][T], or NULL: the token's index t            */
+    const int* pair_axis;    /* DEVICE [rot / 2], each in [0, axes) (others count as the     */
+                             /* nearest); NULL: all on axis 0                                */
+    const float* q_weight;   /* DEVICE [d] norm weights, or NULL: no norm of queries         */
+    const float* k_weight;   /* the same for keys                                            */
+} forge_qkv_config;
+
+/* A projection-side tensor [B][T][heads][d] of 16-bit values, d contiguous, the other
+ * strides in elements: slices of one packed [B][T][H + 2 Hkv][d] projection, or tensors of
+ * their own.  data 16-byte aligned, strides multiples of 8 (those of a dimension of size
+ * one are not looked at); sources may repeat elements (stride 0). */
+typedef struct {
+    const void* data; /* written where it is a gradient */
+    long long stride_b, stride_t, stride_h;
+} forge_qkv_tensor;
+
+/*
+ * Forward.  q, k, v: the projection's tensors (H, Hkv and Hkv heads), bf16 or fp16 with
+ * FORGE_ATTN_FP16; q_out, k_out, v_out: contiguous [B][H][T][d] of the same type, as
+ * forge_attn_fwd reads them.  A tensor and its output may both be NULL (left out).
+ * B * T * H * d < 2^31.  One launch; deterministic.  flags: FORGE_ATTN_FP16,
+ * FORGE_QKV_ADJACENT.
+ */
+int forge_qkv_fwd(const forge_qkv_config* config, const forge_qkv_tensor* q,
+                  const forge_qkv_tensor* k, const forge_qkv_tensor* v, void* q_out, void* k_out,
+                  void* v_out, int flags, void* stream);
+
+/* Bytes of device workspace forge_qkv_bwd needs on the current device for head dimension d
+ * (0 if it is not 64 or 128); only read where a norm weight is given. */
+size_t forge_qkv_bwd_workspace_size(int d);
+
+/*
+ * Backward of forge_qkv_fwd with the same config.  dq, dk, dv: gradients of its outputs,
+ * contiguous [B][H][T][d], 16-bit or fp32 (FORGE_QKV_GRAD_F32).  q, k: its inputs (read
+ * only where their weight is given, else they may be NULL).  q_grad, k_grad, v_grad: where
+ * the projection's gradients go, 16-bit, laid out like its tensors; their elements must not
+ * coincide (checked within each tensor).  A gradient and its output may both be NULL.
+ * dq_weight, dk_weight: fp32 [d], required where the weight is given; accumulate = 1 adds
+ * to their contents.  The gradients of shared key / value heads are summed in fp32 before
+ * anything is rounded.  One launch, and a small second one where a norm weight is given;
+ * deterministic (no atomics).  workspace: 16-byte aligned, contents unspecified on entry and
+ * on return.  flags: FORGE_ATTN_FP16, FORGE_QKV_ADJACENT, FORGE_QKV_GRAD_F32.
+ */
+int forge_qkv_bwd(const forge_qkv_config* config, const void* dq, const void* dk, const void* dv,
+                  const forge_qkv_tensor* q, const forge_qkv_tensor* k,
+                  const forge_qkv_tensor* q_grad, const forge_qkv_tensor* k_grad,
+                  const forge_qkv_tensor* v_grad, float* dq_weight, float* dk_weight,
+                  int accumulate, void* workspace, size_t workspace_bytes, int flags,
+                  void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* forge_attn_status_string(int status);
 

@@ -59,6 +59,37 @@ int forge_linear_bwd_dw(const void* dy, const void* x, float* dw, int tokens, in
  * forge_linear_bwd_dw would reject. */
 int forge_linear_split_k(int tokens, int in_features, int out_features);
 
+/*
+ * The same products grouped by expert (the layers of a mixture of experts, whose tokens a
+ * router has sorted by expert).  offsets: DEVICE int [experts + 1], nondecreasing: the
+ * rows [offsets[e], offsets[e + 1]) of the token matrices belong to expert e, any number of
+ * them, none included.  They are read on the device only; each is clamped to [0, rows], so
+ * that no contents can lead outside the tensors.  rows: the token matrices' rows; those that
+ * belong to no expert are not read as data and not written.  Rows need not be a multiple of
+ * anything; in_features and out_features are multiples of 8; experts <= 1024.
+ *   w, dw [experts][out_features][in_features]; each matrix, and each token matrix, below
+ *   2^31 elements.
+ * rows = 0 is allowed (x, dy, y, dx may then be NULL).  Other conventions as above.  One launch
+ * each (a memset for dw when rows = 0); deterministic.
+ */
+#define FORGE_LINEAR_MAX_EXPERTS 1024
+
+/* y[r] = x[r] w_e^T for the rows r of each expert e.  flags: FORGE_ATTN_OUT_F32, FORGE_ATTN_FP16. */
+int forge_linear_grouped_fwd(const void* x, const void* w, void* y, const int* offsets, int rows,
+                             int experts, int in_features, int out_features, int flags,
+                             void* stream);
+
+/* dx[r] = dy[r] w_e for the rows r of each expert e.  flags as for the forward. */
+int forge_linear_grouped_bwd_dx(const void* dy, const void* w, void* dx, const int* offsets,
+                                int rows, int experts, int in_features, int out_features, int flags,
+                                void* stream);
+
+/* dw_e = sum over expert e's rows of dy[r]^T x[r], fp32; accumulate = 1 adds to dw's contents.
+ * An expert without rows gets zeros (accumulate: keeps its contents).  flags: FORGE_ATTN_FP16. */
+int forge_linear_grouped_bwd_dw(const void* dy, const void* x, float* dw, const int* offsets,
+                                int rows, int experts, int in_features, int out_features,
+                                int accumulate, int flags, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,3 +35,24 @@ def linear_bwd_dx(dy, w):
 def linear_bwd_dw(dy, x):
     """dW = dY^T X.  dy: [tokens, out], x: [tokens, in] -> [out, in]."""
     return np.asarray(dy, dtype=np.float64).T @ np.asarray(x, dtype=np.float64)
+
+
+# The same products grouped by expert: rows [offsets[e], offsets[e + 1]) belong to expert e.
+def grouped_fwd(x, w, offsets):
+    """Rows that belong to no expert are NaN.  w: [experts, out, in]."""
+    y = np.full((len(x), w.shape[1]), np.nan)
+    for e, (a, b) in enumerate(zip(offsets[:-1], offsets[1:])):
+        y[a:b] = linear_fwd(x[a:b], w[e])
+    return y
+
+
+def grouped_bwd_dx(dy, w, offsets):
+    """Rows that belong to no expert are NaN."""
+    dx = np.full((len(dy), w.shape[2]), np.nan)
+    for e, (a, b) in enumerate(zip(offsets[:-1], offsets[1:])):
+        dx[a:b] = linear_bwd_dx(dy[a:b], w[e])
+    return dx
+
+
+def grouped_bwd_dw(dy, x, offsets):
+    return np.stack([linear_bwd_dw(dy[a:b], x[a:b]) for a, b in zip(offsets[:-1], offsets[1:])])
