@@ -13,9 +13,9 @@
 // Bound by HBM: each value is read once and written once (a shared head is written once
 // for each of its copies).  D / 16 threads hold a head of a token, 16 values each: two
 // 16-byte chunks placed so that both members of every rotated pair are in one thread.
-// A block takes 8 consecutive tokens and a run of heads, computes the tokens' sines and
-// cosines once into shared memory, and keeps a thread at its token, so that the angles
-// stay in registers while it walks the heads.  Angles are reduced in 64 bits (turns =
+// A block takes 16 consecutive tokens and a run of heads of q, k or v, computes the tokens'
+// sines and cosines once into shared memory, and keeps each thread at its token while it
+// walks the heads.  Angles are reduced in 64 bits (turns =
 // position * f / 2 pi, minus the nearest integer): a 32-bit product would lose the phase
 // of far positions altogether.
 #include <cmath>
@@ -28,14 +28,13 @@ namespace forge {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTok = 8;   // tokens per block
-constexpr int kUnroll = 4;  // head rows a thread has in flight
+constexpr int kTok = 16;  // tokens per block
 
 struct Rope {
     const double* freq;  // [pairs]
     const int* pos;      // [axes][B * T], or null: the token's index t
     const int* axis;     // [pairs], or null: axis 0
-    int pairs, axes, adjacent;
+    int pairs, axes;
 };
 
 // One of q, k, v: `heads` heads in the projection's layout, each going to `rep` heads of
@@ -55,8 +54,8 @@ struct Parts {
 };
 
 struct Shape {
-    int B, T, H;
-    long long tokens;
+    int T, H;
+    unsigned tokens;
     float eps;
 };
 
@@ -69,80 +68,93 @@ struct Cfg {
 
 // First elements of the two 8-element chunks of thread i of a row: the halves of the
 // same eight pairs while those last, then neighbours (elements that are not rotated).
-__device__ __forceinline__ void chunks_of(int i, const Rope& r, int& a, int& b) {
-    const int half = r.pairs >> 3;
-    if (r.adjacent) {
-        a = 16 * i;
-        b = a + 8;
-    } else if (i < half) {
+template <bool ADJ>
+__device__ __forceinline__ void chunks_of(int i, int pairs, int& a, int& b) {
+    if (!ADJ && 8 * i < pairs) {
         a = 8 * i;
-        b = a + r.pairs;
+        b = a + pairs;
     } else {
         a = 16 * i;
         b = a + 8;
     }
 }
 
-// (cos, sin) of the block's tokens and all pairs, [kTok][pairs].
-__device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, long long tok0,
-                                            float2* cs) {
-    const int n = kTok * r.pairs;
-    for (int k = threadIdx.x; k < n; k += kThreads) {
-        const int t = k / r.pairs, j = k - t * r.pairs;
-        const long long tok = tok0 + t;
+// Tables in shared memory: what thread i of a row reads lies in four 16-byte columns, each
+// with the threads of a row side by side.
+// Angles, [kTok][4][kLanes] of (cos, cos, sin, sin) of two pairs.  A warp takes two tokens.
+template <int D>
+__device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsigned tok0,
+                                            float* cs) {
+    constexpr int L = Cfg<D>::kLanes;
+    for (unsigned t = warp_id(); t < kTok; t += kThreads / 32) {
+        const unsigned tok = tok0 + t;
         if (tok >= s.tokens) break;
-        const int ax = r.axis ? min(max(r.axis[j], 0), r.axes - 1) : 0;
-        const int p = r.pos ? r.pos[ax * s.tokens + tok] : (int)(tok % s.T);
-        double turns = (double)p * (r.freq[j] * 0.15915494309189533577);
-        turns -= rint(turns);
-        float sn, c;
-        sincospif(2.f * (float)turns, &sn, &c);
-        cs[k] = make_float2(c, sn);
+        const int index = r.pos ? 0 : (int)(tok % (unsigned)s.T);
+        for (int j = lane_id(); j < r.pairs; j += 32) {
+            const int ax = r.axis ? min(max(__ldg(r.axis + j), 0), r.axes - 1) : 0;
+            const int p = r.pos ? __ldg(r.pos + (size_t)ax * s.tokens + tok) : index;
+            double turns = (double)p * (__ldg(r.freq + j) * 0.15915494309189533577);
+            turns -= rint(turns);
+            float sn, c;
+            sincospif(2.f * (float)turns, &sn, &c);
+            float* at = cs + ((t * 4 + (j & 7) / 2) * L + j / 8) * 4 + (j & 1);
+            at[0] = c;
+            at[2] = sn;
+        }
+    }
+}
+// Norm weights, [4][kLanes] of four: the thread's chunks a and b.
+template <int D, bool ADJ>
+__device__ __forceinline__ void fill_weights(const float* w, int pairs, float* out) {
+    constexpr int L = Cfg<D>::kLanes;
+    if (threadIdx.x < D) {
+        const int i = threadIdx.x % L, c = threadIdx.x / L;  // element c of the 16 of thread i
+        int a, b;
+        chunks_of<ADJ>(i, pairs, a, b);
+        out[((c / 4) * L + i) * 4 + c % 4] = w[(c < 8 ? a : b - 8) + c];
     }
 }
 
-// The (cos, sin) of the thread's pairs; returns how many of its eight there are.
-__device__ __forceinline__ int load_angles(const Rope& r, const float2* cs, int t, int i,
-                                           float2* c8) {
-    const int n = min(max(r.pairs - 8 * i, 0), 8);
-    const float2* p = cs + t * r.pairs + 8 * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) c8[j] = p[j];
-    return n;
-}
-
+// A thread's 16 values of a row: chunk a in the first four pairs, chunk b in the others.
+// Arithmetic goes by pairs (f32x2 instructions): the kernels are close to the issue limit.
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 p = unpack16x2<F16>(w[j]);
-        f[2 * j] = p.x;
-        f[2 * j + 1] = p.y;
-    }
+__device__ __forceinline__ void unpack8(const uint4& u, float2* f) {
+    f[0] = unpack16x2<F16>(u.x);
+    f[1] = unpack16x2<F16>(u.y);
+    f[2] = unpack16x2<F16>(u.z);
+    f[3] = unpack16x2<F16>(u.w);
 }
 template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3]),
-                      pack16x2<F16>(f[4], f[5]), pack16x2<F16>(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+    return make_uint4(pack16x2<F16>(f[0].x, f[0].y), pack16x2<F16>(f[1].x, f[1].y),
+                      pack16x2<F16>(f[2].x, f[2].y), pack16x2<F16>(f[3].x, f[3].y));
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Rotates the thread's first n pairs (inverse: by -phi); the other values stay as they are.
-template <bool INVERSE>
-__device__ __forceinline__ void rotate(float* x, const float2* c8, int n, int adjacent) {
+// Rotates the thread's first n pairs (inverse: by -phi); the other values stay as they are
+// (not multiplied by one and zero: a neighbour may be infinite).  cs: the thread's column of
+// its token.
+template <int L, bool ADJ, bool INVERSE>
+__device__ __forceinline__ void rotate(float2* x, const float4* cs, int n) {
+    if (n <= 0) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j >= n) break;
-        const float c = c8[j].x, s = INVERSE ? -c8[j].y : c8[j].y;
-        if (adjacent) {
-            const float a = x[2 * j], b = x[2 * j + 1];
-            x[2 * j] = a * c - b * s;
-            x[2 * j + 1] = a * s + b * c;
-        } else {
-            const float a = x[j], b = x[8 + j];
-            x[j] = a * c - b * s;
-            x[8 + j] = a * s + b * c;
+    for (int c = 0; c < 4; ++c) {
+        const float4 v = cs[c * L];
+        const float2 co = make_float2(v.x, v.y);
+        const float2 up = INVERSE ? make_float2(-v.z, -v.w) : make_float2(v.z, v.w);
+        const float2 dn = INVERSE ? make_float2(v.z, v.w) : make_float2(-v.z, -v.w);
+        if constexpr (ADJ) {
+            const float2 p = x[2 * c], q = x[2 * c + 1];
+            const float2 p2 = ffma2(make_float2(p.y, p.x), make_float2(dn.x, up.x),
+                                    fmul2(p, both(co.x)));
+            const float2 q2 = ffma2(make_float2(q.y, q.x), make_float2(dn.y, up.y),
+                                    fmul2(q, both(co.y)));
+            if (2 * c < n) x[2 * c] = p2;
+            if (2 * c + 1 < n) x[2 * c + 1] = q2;
+        } else {  // halves come in eights: all of the thread's pairs or none
+            const float2 a = x[c], b = x[4 + c];
+            x[c] = ffma2(b, dn, fmul2(a, co));
+            x[4 + c] = ffma2(a, up, fmul2(b, co));
         }
     }
 }
@@ -155,221 +167,302 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// A block to each (token tile, run of heads); runs of `per` heads of q, then k, then v.
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads)
+// Copies go through a ring in shared memory, each thread's own 16-byte slots: kDepth rows
+// are in flight without a register or a barrier spent on them.  (With the rows in registers
+// instead, two blocks fitted on an SM and the forward at B1 T8000 H32 d128 took 104.5 us.)
+// Where there is no row (on = false) the slot gets zeros and nothing is read.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kFwdDepth = 4;
+
+// Runs of heads that the blocks of a token tile take: nq runs of q's heads, nk of k's and the
+// rest of v's, `per` heads to a run.
+template <int D, bool F16, bool ADJ>
+__global__ void __launch_bounds__(kThreads, 4)
     qkv_fwd_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int nq, int nk,
                    int runs, int per) {
     using C = Cfg<D>;
-    __shared__ float2 cs[kTok * D / 2];
-    const int tile = (int)(blockIdx.x / (unsigned)runs);
-    int run = (int)(blockIdx.x % (unsigned)runs);
+    constexpr int L = C::kLanes;
+    __shared__ float4 cs[kTok * 4 * L];
+    __shared__ float4 wt[4 * L];
+    __shared__ uint4 ring[kFwdDepth][2][kThreads];
+    const unsigned tile = blockIdx.x / (unsigned)runs;
+    int run = (int)(blockIdx.x - tile * (unsigned)runs);
     const int kind = run < nq ? 0 : (run < nq + nk ? 1 : 2);
-    const Part& p = parts.part[kind];
     run -= kind == 0 ? 0 : (kind == 1 ? nq : nq + nk);
-    const long long tok0 = (long long)tile * kTok;
-    const int i = threadIdx.x % C::kLanes, g = threadIdx.x / C::kLanes;
+    const Part& p = parts.part[kind];
+    const unsigned tok0 = tile * kTok;
+    const int i = threadIdx.x % L, g = threadIdx.x / L;
     const int t = g % kTok, slot = g / kTok;
-    const long long tok = tok0 + t;
-    const bool live = tok < s.tokens;
-    const bool turn = kind < 2 && rope.pairs > 0;
+    const unsigned tok = min(tok0 + t, s.tokens - 1);
+    const unsigned b = tok / (unsigned)s.T, tt = tok - b * (unsigned)s.T;
     int ea, eb;
-    chunks_of(i, rope, ea, eb);
-    const long long b = tok / s.T, tt = tok - b * s.T;
-    const uint16_t* x = static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st;
-    uint16_t* y = static_cast<uint16_t*>(p.y) + (b * s.H * s.T + tt) * D;
-    if (turn) fill_angles(rope, s, tok0, cs);
-    float2 c8[8];
-    float w[16];
-    if (kind < 2 && p.w) {
+    chunks_of<ADJ>(i, rope.pairs, ea, eb);
+    const int first = run * per + slot;
+    // heads this thread may take, counted from `first` (none where its token is not there)
+    const int mine = tok0 + t < s.tokens ? min((run + 1) * per, p.heads) - first : 0;
+    const int rows = (min((run + 1) * per, p.heads) - run * per + C::kSlots - 1) / C::kSlots;
+
+    const uint16_t* x =
+        static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st + (mine > 0 ? first * p.sh : 0);
+    const long long x_step = C::kSlots * p.sh;
+    int fetched = 0;  // heads, in steps of kSlots
+    auto prefetch = [&](int at) {
+        const bool on = fetched < mine;
+        copy16(&ring[at][0][threadIdx.x], x + ea, on);
+        copy16(&ring[at][1][threadIdx.x], x + eb, on);
+        copies_commit();
+        fetched += C::kSlots;
+        if (fetched < mine) x += x_step;  // (past the last row the address stays valid)
+    };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[j] = p.w[ea + j];
-            w[8 + j] = p.w[eb + j];
-        }
-    }
+    for (int n = 0; n < kFwdDepth; ++n) prefetch(n);
+    const bool norm = kind < 2 && p.w != nullptr;
+    if (kind < 2 && rope.pairs > 0) fill_angles<D>(rope, s, tok0, reinterpret_cast<float*>(cs));
+    if (norm) fill_weights<D, ADJ>(p.w, rope.pairs, reinterpret_cast<float*>(wt));
     __syncthreads();
-    const int n8 = turn ? load_angles(rope, cs, t, i, c8) : 0;
-    const int h1 = min((run + 1) * per, p.heads);
-    for (int h0 = run * per + slot; h0 - slot < h1; h0 += C::kSlots * kUnroll) {
-        uint4 in[kUnroll][2];
+    const int n8 = rope.pairs - 8 * i;  // the thread's rotated pairs (at most eight count)
+    const float4* my_cs = cs + t * 4 * L + i;
+    const long long head = (long long)s.T * D;
+    uint16_t* y = static_cast<uint16_t*>(p.y) +
+                  (((long long)b * s.H + (long long)first * p.rep) * s.T + tt) * D;
+
+    for (int n = 0; n < rows; ++n) {
+        copies_wait<kFwdDepth - 1>();
+        uint4* at = &ring[n % kFwdDepth][0][threadIdx.x];
+        uint4 oa = at[0], ob = at[kThreads];
+        if (kind < 2) {
+            float2 f[8];
+            unpack8<F16>(oa, f);
+            unpack8<F16>(ob, f + 4);
+            if (norm) {
+                float2 ss = fmul2(f[0], f[0]);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + u * C::kSlots;
-            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
-            if (live && h < h1) {
-                in[u][0] = __ldg(reinterpret_cast<const uint4*>(x + h * p.sh + ea));
-                in[u][1] = __ldg(reinterpret_cast<const uint4*>(x + h * p.sh + eb));
-            }
-        }
+                for (int j = 1; j < 8; ++j) ss = ffma2(f[j], f[j], ss);
+                const float2 r = both(rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + s.eps));
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + u * C::kSlots;
-            uint4 oa = in[u][0], ob = in[u][1];
-            if (kind < 2) {
-                float f[16];
-                unpack8<F16>(oa, f);
-                unpack8<F16>(ob, f + 8);
-                if (p.w) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) ss = fmaf(f[j], f[j], ss);
-                    const float r = rsqrtf(row_sum<C::kLanes>(ss) * (1.f / D) + s.eps);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = f[j] * r * w[j];
-                }
-                if (turn) rotate<false>(f, c8, n8, rope.adjacent);
-                oa = pack8<F16>(f);
-                ob = pack8<F16>(f + 8);
-            }
-            if (live && h < h1) {
-                for (int c = 0; c < p.rep; ++c) {
-                    uint16_t* o = y + (long long)(h * p.rep + c) * s.T * D;
-                    *reinterpret_cast<uint4*>(o + ea) = oa;
-                    *reinterpret_cast<uint4*>(o + eb) = ob;
+                for (int c = 0; c < 4; ++c) {
+                    const float4 w = wt[c * L + i];
+                    f[2 * c] = fmul2(fmul2(f[2 * c], r), make_float2(w.x, w.y));
+                    f[2 * c + 1] = fmul2(fmul2(f[2 * c + 1], r), make_float2(w.z, w.w));
                 }
             }
+            rotate<L, ADJ, false>(f, my_cs, n8);
+            oa = pack8<F16>(f);
+            ob = pack8<F16>(f + 4);
         }
+        if (n * C::kSlots < mine) {
+            for (int c = 0; c < p.rep; ++c, y += head) {
+                *reinterpret_cast<uint4*>(y + ea) = oa;
+                *reinterpret_cast<uint4*>(y + eb) = ob;
+            }
+            y += (C::kSlots - 1) * p.rep * head;
+        }
+        prefetch(n % kFwdDepth);  // into the slots just read
     }
+    copies_wait<0>();
 }
 
-// The thread's 16 gradients of a row on the attention's side, in 32 bits.
-template <bool F16, bool G32>
-__device__ __forceinline__ void add_grad(const void* g, long long off, int ea, int eb, float* f) {
-    if constexpr (G32) {
-        const float* p = static_cast<const float*>(g) + off;
-        const float4 v[4] = {__ldg(reinterpret_cast<const float4*>(p + ea)),
-                             __ldg(reinterpret_cast<const float4*>(p + ea) + 1),
-                             __ldg(reinterpret_cast<const float4*>(p + eb)),
-                             __ldg(reinterpret_cast<const float4*>(p + eb) + 1)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[4 * j] += v[j].x;
-            f[4 * j + 1] += v[j].y;
-            f[4 * j + 2] += v[j].z;
-            f[4 * j + 3] += v[j].w;
-        }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(g) + off;
-        float a[16];
-        unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + ea)), a);
-        unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(p + eb)), a + 8);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] += a[j];
-    }
-}
+// The ring of the backward: per step one gradient row (16 values: two or four slots) and the
+// row of x (two slots).
+template <bool G32>
+struct Bwd {
+    static constexpr int kG = G32 ? 4 : 2;
+    static constexpr int kDepth = G32 ? 3 : 4;
+    static constexpr int kRingBytes = kDepth * (kG + 2) * kThreads * 16;
+    static constexpr int kBlocksPerSm = G32 ? 2 : 3;  // what shared memory holds
+};
+constexpr int kMaxBwdBlocksPerSm = 3;
 
 // Blocks [0, nq) walk q's (token tile, run of heads) units, the next nk k's, the rest v's.
-// Each block of q and k sums its share of the norm weight's gradient in registers and
-// writes it to partials[block][D].
-template <int D, bool F16, bool G32>
-__global__ void __launch_bounds__(kThreads)
+// A head row takes p.rep steps, one for each of the attention's heads that share it; the
+// norm's backward follows the last.  Each block of q and k sums its share of the norm
+// weight's gradient in registers and writes it to partials[block][D].
+template <int D, bool F16, bool G32, bool ADJ>
+__global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
     qkv_bwd_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int nq, int nk,
                    int per, float* __restrict__ partials) {
     using C = Cfg<D>;
-    __shared__ float2 cs[kTok * D / 2];
-    int blk = blockIdx.x;
-    const int kind = blk < nq ? 0 : (blk < nq + nk ? 1 : 2);
+    using R = Bwd<G32>;
+    constexpr int L = C::kLanes;
+    constexpr int kStep = (R::kG + 2) * kThreads;
+    extern __shared__ uint4 ring[];  // [kDepth][kG + 2][kThreads]
+    __shared__ float4 cs[kTok * 4 * L];
+    __shared__ float4 wt[4 * L];
+    allow_dependents_launch();
+    unsigned blk = blockIdx.x;
+    const int kind = (int)blk < nq ? 0 : ((int)blk < nq + nk ? 1 : 2);
     const Part& p = parts.part[kind];
     blk -= kind == 0 ? 0 : (kind == 1 ? nq : nq + nk);
-    const int blocks = kind == 0 ? nq : (kind == 1 ? nk : (int)gridDim.x - nq - nk);
-    const int i = threadIdx.x % C::kLanes, g = threadIdx.x / C::kLanes;
+    const unsigned blocks = kind == 0 ? nq : (kind == 1 ? nk : gridDim.x - nq - nk);
+    const int i = threadIdx.x % L, g = threadIdx.x / L;
     const int t = g % kTok, slot = g / kTok;
     const bool turn = kind < 2 && rope.pairs > 0;
     const bool norm = kind < 2 && p.w != nullptr;
     int ea, eb;
-    chunks_of(i, rope, ea, eb);
-    float w[16], dw[16];
-    if (norm) {
+    chunks_of<ADJ>(i, rope.pairs, ea, eb);
+    if (norm) fill_weights<D, ADJ>(p.w, rope.pairs, reinterpret_cast<float*>(wt));
+    float2 dw[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[j] = p.w[ea + j];
-            w[8 + j] = p.w[eb + j];
-        }
-    }
+    for (int j = 0; j < 8; ++j) dw[j] = both(0.f);
+    const unsigned runs = (unsigned)((p.heads + per - 1) / per);
+    const unsigned units = (s.tokens + kTok - 1) / kTok * runs;
+    const int n8 = turn ? rope.pairs - 8 * i : 0;
+    const float4* my_cs = cs + t * 4 * L + i;
+    const long long head = (long long)s.T * D;  // from one of the attention's heads to the next
+    const long long x_step = C::kSlots * p.sh, y_step = C::kSlots * p.gsh;
+    uint4* const ring0 = ring + threadIdx.x;
+
+    for (unsigned unit = blk; unit < units; unit += blocks) {
+        const unsigned tok0 = unit / runs * kTok;
+        const int h0 = (int)(unit % runs) * per, first = h0 + slot;
+        const int last = min(h0 + per, p.heads);
+        const unsigned tok = min(tok0 + t, s.tokens - 1);
+        const unsigned b = tok / (unsigned)s.T, tt = tok - b * (unsigned)s.T;
+        const int mine = tok0 + t < s.tokens ? last - first : 0;
+        const long long at_first = mine > 0 ? first : 0;
+        const uint16_t* x =
+            static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st + at_first * p.sh;
+        uint16_t* y = static_cast<uint16_t*>(p.y) + b * p.gsb + tt * p.gst + at_first * p.gsh;
+        const char* dy = static_cast<const char*>(p.g) +
+                         (((long long)b * s.H + at_first * p.rep) * s.T + tt) * (D * (G32 ? 4 : 2));
+        int fetched = 0, shared_head = 0;  // heads in steps of kSlots; which of the rep rows
+        int pf_at = 0;
+        auto prefetch = [&]() {
+            uint4* at = ring0 + pf_at;
+            pf_at = pf_at == (R::kDepth - 1) * kStep ? 0 : pf_at + kStep;
+            const bool on = fetched < mine;
+            if constexpr (G32) {
+                const float* src = reinterpret_cast<const float*>(dy);
+                copy16(at, src + ea, on);
+                copy16(at + kThreads, src + ea + 4, on);
+                copy16(at + 2 * kThreads, src + eb, on);
+                copy16(at + 3 * kThreads, src + eb + 4, on);
+            } else {
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(dy);
+                copy16(at, src + ea, on);
+                copy16(at + kThreads, src + eb, on);
+            }
+            // the row's last step brings its x, and goes on to the next row
+            if (++shared_head == p.rep) {
+                if (norm) {
+                    copy16(at + R::kG * kThreads, x + ea, on);
+                    copy16(at + (R::kG + 1) * kThreads, x + eb, on);
+                }
+                shared_head = 0;
+                fetched += C::kSlots;
+                if (fetched < mine) {  // (past the last row the addresses stay valid)
+                    dy += ((C::kSlots - 1) * p.rep + 1) * head * (G32 ? 4 : 2);
+                    x += x_step;
+                }
+            } else if (on) {
+                dy += head * (G32 ? 4 : 2);
+            }
+            copies_commit();
+        };
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dw[j] = 0.f;
-    const int runs = (p.heads + per - 1) / per;
-    const long long tiles = (s.tokens + kTok - 1) / kTok;
-    for (long long unit = blk; unit < tiles * runs; unit += blocks) {
-        const long long tok0 = unit / runs * kTok;
-        const int run = (int)(unit % runs);
-        const long long tok = tok0 + t;
-        const bool live = tok < s.tokens;
-        const long long b = tok / s.T, tt = tok - b * s.T;
-        const uint16_t* x = static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st;
-        uint16_t* y = static_cast<uint16_t*>(p.y) + b * p.gsb + tt * p.gst;
-        const long long grow = (b * s.H * s.T + tt) * D;
-        float2 c8[8];
-        int n8 = 0;
+        for (int n = 0; n < R::kDepth; ++n) prefetch();
         if (turn) {
             __syncthreads();  // the previous unit's angles have been read
-            fill_angles(rope, s, tok0, cs);
-            __syncthreads();
-            n8 = load_angles(rope, cs, t, i, c8);
+            fill_angles<D>(rope, s, tok0, reinterpret_cast<float*>(cs));
         }
-        const int h1 = min((run + 1) * per, p.heads);
-        for (int h0 = run * per + slot; h0 - slot < h1; h0 += C::kSlots) {
-            const bool on = live && h0 < h1;
-            float f[16];
+        __syncthreads();
+        int at_now = 0;
+        const int rows = (last - h0 + C::kSlots - 1) / C::kSlots;
+        for (int row = 0; row < rows; ++row) {
+            float2 f[8];
+            const uint4* at;
+            for (int c = 0;;) {
+                copies_wait<R::kDepth - 1>();
+                at = ring0 + at_now;
+                at_now = at_now == (R::kDepth - 1) * kStep ? 0 : at_now + kStep;
+                float2 a[8];
+                if constexpr (G32) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = 0.f;
-            uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-            if (on) {
-                if (norm) {
-                    xa = __ldg(reinterpret_cast<const uint4*>(x + h0 * p.sh + ea));
-                    xb = __ldg(reinterpret_cast<const uint4*>(x + h0 * p.sh + eb));
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 v = at[q * kThreads];
+                        a[2 * q] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+                        a[2 * q + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+                    }
+                } else {
+                    unpack8<F16>(at[0], a);
+                    unpack8<F16>(at[kThreads], a + 4);
                 }
-                for (int c = 0; c < p.rep; ++c)
-                    add_grad<F16, G32>(p.g, grow + (long long)(h0 * p.rep + c) * s.T * D, ea, eb, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = c == 0 ? a[j] : fadd2(f[j], a[j]);
+                if (++c == p.rep) break;
+                prefetch();
             }
-            if (turn) rotate<true>(f, c8, n8, rope.adjacent);
+            rotate<L, ADJ, true>(f, my_cs, n8);
             if (norm) {
-                float n[16];
-                unpack8<F16>(xa, n);
-                unpack8<F16>(xb, n + 8);
-                float ss = 0.f, dot = 0.f;
+                // dx = r (u - n mean(u n)) with n = r x, u = g w: both row sums at once
+                float2 x2[8];
+                unpack8<F16>(at[R::kG * kThreads], x2);
+                unpack8<F16>(at[(R::kG + 1) * kThreads], x2 + 4);
+                float2 ss = both(0.f), ux = both(0.f), u[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    ss = fmaf(n[j], n[j], ss);
-                    dot = fmaf(f[j] * w[j], n[j], dot);
+                for (int c = 0; c < 4; ++c) {
+                    const float4 w = wt[c * L + i];
+                    u[2 * c] = fmul2(f[2 * c], make_float2(w.x, w.y));
+                    u[2 * c + 1] = fmul2(f[2 * c + 1], make_float2(w.z, w.w));
                 }
-                const float r = rsqrtf(row_sum<C::kLanes>(ss) * (1.f / D) + s.eps);
-                const float m = row_sum<C::kLanes>(dot) * r * (1.f / D);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    n[j] *= r;
-                    dw[j] = fmaf(f[j], n[j], dw[j]);
-                    f[j] = r * (f[j] * w[j] - n[j] * m);
+                for (int j = 0; j < 8; ++j) {
+                    ss = ffma2(x2[j], x2[j], ss);
+                    ux = ffma2(u[j], x2[j], ux);
+                }
+                const float r = rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + s.eps);
+                const float m = row_sum<L>(ux.x + ux.y) * r * (1.f / D);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 n = fmul2(x2[j], both(r));
+                    dw[j] = ffma2(f[j], n, dw[j]);
+                    f[j] = fmul2(ffma2(n, both(-m), u[j]), both(r));
                 }
             }
-            if (on) {
-                *reinterpret_cast<uint4*>(y + h0 * p.gsh + ea) = pack8<F16>(f);
-                *reinterpret_cast<uint4*>(y + h0 * p.gsh + eb) = pack8<F16>(f + 8);
+            if (row * C::kSlots < mine) {
+                *reinterpret_cast<uint4*>(y + ea) = pack8<F16>(f);
+                *reinterpret_cast<uint4*>(y + eb) = pack8<F16>(f + 4);
+                y += y_step;
             }
+            prefetch();
         }
     }
+    copies_wait<0>();
     if (norm) {
         // the block's sum, always added in the same order
-        __shared__ float red[kThreads / 32][D];
+        __syncthreads();
+        float* red = reinterpret_cast<float*>(ring);  // [warps][D]
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 8; ++j) {
 #pragma unroll
-            for (int o = C::kLanes; o < 32; o <<= 1)
-                dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
-        if ((threadIdx.x & 31) < C::kLanes) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                red[threadIdx.x >> 5][ea + j] = dw[j];
-                red[threadIdx.x >> 5][eb + j] = dw[8 + j];
+            for (int o = L; o < 32; o <<= 1) {
+                dw[j].x += __shfl_xor_sync(0xffffffffu, dw[j].x, o);
+                dw[j].y += __shfl_xor_sync(0xffffffffu, dw[j].y, o);
+            }
+            if (lane_id() < L) {
+                const int e = j < 4 ? ea + 2 * j : eb + 2 * (j - 4);
+                red[warp_id() * D + e] = dw[j].x;
+                red[warp_id() * D + e + 1] = dw[j].y;
             }
         }
         __syncthreads();
         if (threadIdx.x < D) {
             float sum = 0.f;
 #pragma unroll
-            for (int wv = 0; wv < kThreads / 32; ++wv) sum += red[wv][threadIdx.x];
-            partials[(long long)blockIdx.x * D + threadIdx.x] = sum;
+            for (int wv = 0; wv < kThreads / 32; ++wv) sum += red[wv * D + threadIdx.x];
+            partials[(size_t)blockIdx.x * D + threadIdx.x] = sum;
         }
     }
 }
@@ -380,6 +473,7 @@ constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(8 * kSumRows)
     qkv_dw_kernel(const float* __restrict__ partials, float* dwq, float* dwk, int nq, int nk, int D,
                   int accumulate) {
+    grid_dependency_wait();
     float* out = blockIdx.y == 0 ? dwq : dwk;
     if (!out) return;
     const int first = blockIdx.y == 0 ? 0 : nq, n = blockIdx.y == 0 ? nq : nk;
@@ -449,14 +543,13 @@ int check_config(const forge_qkv_config* c, int flags, int allowed) {
     return FORGE_ATTN_OK;
 }
 
-Rope make_rope(const forge_qkv_config& c, int flags) {
+Rope make_rope(const forge_qkv_config& c) {
     Rope r;
     r.freq = c.inv_freq;
     r.pos = c.positions;
     r.axis = c.pair_axis;
     r.pairs = c.rot / 2;
     r.axes = c.axes;
-    r.adjacent = (flags & FORGE_QKV_ADJACENT) != 0;
     return r;
 }
 
@@ -474,14 +567,12 @@ Part make_part(const forge_qkv_tensor* x, const float* w, int heads, int rep) {
     return p;
 }
 
-// Blocks of the backward: two to an SM, shared out among q, k and v by the bytes each
-// moves, at least one to a part that is there and no more than it has units.
-constexpr int kBwdBlocksPerSm = 2;
+// Blocks of the backward: as many as are resident, shared out among q, k and v by the bytes
+// each moves, at least one to a part that is there and no more than it has units.
 struct Blocks {
     int n[3];
 };
-Blocks share_out(const double* bytes, const long long* units) {
-    const int all = kBwdBlocksPerSm * sm_count();
+Blocks share_out(const double* bytes, const long long* units, int all) {
     const double sum = bytes[0] + bytes[1] + bytes[2];
     Blocks r;
     for (int j = 0; j < 3; ++j) {
@@ -492,7 +583,34 @@ Blocks share_out(const double* bytes, const long long* units) {
     return r;
 }
 
-int max_bwd_blocks() { return kBwdBlocksPerSm * sm_count() + 3; }
+// Heads of a block's run: eight rows to a thread, fewer (down to one) where that would leave
+// less than `want` blocks.
+int heads_to_a_block(int d, int heads, long long tiles, long long want) {
+    const int slots = d == 64 ? Cfg<64>::kSlots : Cfg<128>::kSlots;
+    int rows = 8;
+    while (rows > 1 && tiles * ((heads + rows * slots - 1) / (rows * slots)) < want) rows /= 2;
+    return rows * slots;
+}
+
+int max_bwd_blocks() { return kMaxBwdBlocksPerSm * sm_count() + 3; }
+
+template <int D, bool F16, bool G32, bool ADJ>
+cudaError_t launch_bwd_t(const Parts& parts, const Rope& rope, const Shape& s, const Blocks& n,
+                         int per, float* ws, cudaStream_t stream) {
+    static std::atomic<unsigned long long> configured{0};
+    auto* kernel = qkv_bwd_kernel<D, F16, G32, ADJ>;
+    cudaError_t e = set_max_dynamic_smem(kernel, Bwd<G32>::kRingBytes, configured);
+    if (e != cudaSuccess) return e;
+    kernel<<<n.n[0] + n.n[1] + n.n[2], kThreads, Bwd<G32>::kRingBytes, stream>>>(
+        parts, rope, s, n.n[0], n.n[1], per, ws);
+    return cudaGetLastError();
+}
+template <int D, bool F16, bool G32>
+cudaError_t launch_bwd(bool adj, const Parts& parts, const Rope& rope, const Shape& s,
+                       const Blocks& n, int per, float* ws, cudaStream_t stream) {
+    return adj ? launch_bwd_t<D, F16, G32, true>(parts, rope, s, n, per, ws, stream)
+               : launch_bwd_t<D, F16, G32, false>(parts, rope, s, n, per, ws, stream);
+}
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? FORGE_ATTN_OK : FORGE_ATTN_ERR_CUDA; }
 
@@ -519,24 +637,29 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
         if ((st = check_strides(*in[j], c->B, c->T, heads[j])) != FORGE_ATTN_OK) return st;
         if (!aligned(out[j], 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
-    const int per = (c->d == 64 ? Cfg<64>::kSlots : Cfg<128>::kSlots) * kUnroll;
+    const long long tokens = (long long)c->B * c->T, tiles = (tokens + kTok - 1) / kTok;
     Parts parts;
-    Part* p = parts.part;
-    int n[3];
+    int all = 0, n[3];
+    for (int j = 0; j < 3; ++j) all += in[j] ? heads[j] : 0;
+    const int per = heads_to_a_block(c->d, all, tiles, 4LL * sm_count());
     for (int j = 0; j < 3; ++j) {
-        p[j] = make_part(in[j], weight[j], heads[j], c->H / heads[j]);
-        p[j].y = out[j];
+        parts.part[j] = make_part(in[j], weight[j], heads[j], c->H / heads[j]);
+        parts.part[j].y = out[j];
         n[j] = in[j] ? (heads[j] + per - 1) / per : 0;
     }
-    const Shape s{c->B, c->T, c->H, (long long)c->B * c->T, c->eps};
-    const Rope rope = make_rope(*c, flags);
+    const Shape s{c->T, c->H, (unsigned)tokens, c->eps};
+    const Rope rope = make_rope(*c);
     const int runs = n[0] + n[1] + n[2];
-    const long long blocks = (s.tokens + kTok - 1) / kTok * runs;
+    const long long blocks = tiles * runs;
     if (blocks > 0x7fffffffll) return FORGE_ATTN_ERR_UNSUPPORTED;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0;
-    auto* kernel = c->d == 64 ? (f16 ? qkv_fwd_kernel<64, true> : qkv_fwd_kernel<64, false>)
-                              : (f16 ? qkv_fwd_kernel<128, true> : qkv_fwd_kernel<128, false>);
+    const bool adj = (flags & FORGE_QKV_ADJACENT) != 0;
+#define FORGE_QKV_FWD(D_)                                                                 \
+    (f16 ? (adj ? qkv_fwd_kernel<D_, true, true> : qkv_fwd_kernel<D_, true, false>)       \
+         : (adj ? qkv_fwd_kernel<D_, false, true> : qkv_fwd_kernel<D_, false, false>))
+    auto* kernel = c->d == 64 ? FORGE_QKV_FWD(64) : FORGE_QKV_FWD(128);
+#undef FORGE_QKV_FWD
     kernel<<<(unsigned)blocks, kThreads, 0, cs>>>(parts, rope, s, n[0], n[1], runs, per);
     return status_of(cudaGetLastError());
 }
@@ -581,10 +704,12 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
         if (!aligned(workspace, 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0, g32 = (flags & FORGE_QKV_GRAD_F32) != 0;
-    const Shape s{c->B, c->T, c->H, (long long)c->B * c->T, c->eps};
-    const Rope rope = make_rope(*c, flags);
-    const int per = (c->d == 64 ? Cfg<64>::kSlots : Cfg<128>::kSlots) * kUnroll;
-    const long long tiles = (s.tokens + kTok - 1) / kTok;
+    const long long tokens = (long long)c->B * c->T, tiles = (tokens + kTok - 1) / kTok;
+    const Shape s{c->T, c->H, (unsigned)tokens, c->eps};
+    const Rope rope = make_rope(*c);
+    const bool adj = (flags & FORGE_QKV_ADJACENT) != 0;
+    const int resident = (g32 ? Bwd<true>::kBlocksPerSm : Bwd<false>::kBlocksPerSm) * sm_count();
+    const int per = heads_to_a_block(c->d, c->H, tiles, resident);
     Parts parts;
     Part* p = parts.part;
     double bytes[3];
@@ -603,24 +728,21 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
         units[j] = out[j] ? tiles * ((heads[j] + per - 1) / per) : 0;
         bytes[j] = out[j] ? (double)c->H * (g32 ? 4 : 2) + heads[j] * (norm ? 4.0 : 2.0) : 0.0;
     }
-    const Blocks n = share_out(bytes, units);
-    const int blocks = n.n[0] + n.n[1] + n.n[2];
+    const Blocks n = share_out(bytes, units, resident);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     float* ws = static_cast<float*>(workspace);
-#define FORGE_QKV_BWD(D_)                                                                       \
-    (f16 ? (g32 ? qkv_bwd_kernel<D_, true, true> : qkv_bwd_kernel<D_, true, false>)             \
-         : (g32 ? qkv_bwd_kernel<D_, false, true> : qkv_bwd_kernel<D_, false, false>))
-    auto* kernel = c->d == 64 ? FORGE_QKV_BWD(64) : FORGE_QKV_BWD(128);
+#define FORGE_QKV_BWD(D_)                                                                \
+    (c->d != D_   ? cudaErrorInvalidValue                                                \
+     : f16 && g32 ? launch_bwd<D_, true, true>(adj, parts, rope, s, n, per, ws, cs)      \
+     : f16        ? launch_bwd<D_, true, false>(adj, parts, rope, s, n, per, ws, cs)     \
+     : g32        ? launch_bwd<D_, false, true>(adj, parts, rope, s, n, per, ws, cs)     \
+                  : launch_bwd<D_, false, false>(adj, parts, rope, s, n, per, ws, cs))
+    cudaError_t e = c->d == 64 ? FORGE_QKV_BWD(64) : FORGE_QKV_BWD(128);
 #undef FORGE_QKV_BWD
-    kernel<<<blocks, kThreads, 0, cs>>>(parts, rope, s, n.n[0], n.n[1], per, ws);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && any_norm) {
-        float* wq = p[0].w ? dq_weight : nullptr;
-        float* wk = p[1].w ? dk_weight : nullptr;
-        qkv_dw_kernel<<<dim3(c->d / 8, 2), 8 * kSumRows, 0, cs>>>(ws, wq, wk, n.n[0], n.n[1], c->d,
-                                                                  accumulate);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && any_norm)
+        e = launch_dependent(qkv_dw_kernel, dim3(c->d / 8, 2), dim3(8 * kSumRows), 0, cs,
+                             (const float*)ws, p[0].w ? dq_weight : nullptr,
+                             p[1].w ? dk_weight : nullptr, n.n[0], n.n[1], c->d, accumulate);
     return status_of(e);
 }
 
