@@ -8,6 +8,7 @@ library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import struct
 
@@ -76,18 +77,6 @@ class QkvTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
                 ("stride_t", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
 
-
-# the same two as bytes, for callers in a hurry (a structure costs the host three times as much)
-_QKV_CONFIG = struct.Struct("7if5P")
-_QKV_TENSOR = struct.Struct("P3q")
-
-
-def qkv_config(B, T, H, Hkv, d, rot, axes, eps, inv_freq, positions, pair_axis, q_weight, k_weight):
-    return _QKV_CONFIG.pack(B, T, H, Hkv, d, rot, axes, eps, inv_freq or 0, positions or 0,
-                            pair_axis or 0, q_weight or 0, k_weight or 0)
-
-
-qkv_tensor = _QKV_TENSOR.pack  # data, stride_b, stride_t, stride_h
 
 # forge_grad_tensor of include/forge_adamw.h: grad, out, n, dtype (padded to 8 bytes)
 _GRAD_TENSOR = "QQqi4x"
@@ -167,6 +156,22 @@ def load(path: str | None = None):
     if path is None:
         _lib = lib
     return lib
+
+
+_front = None
+
+
+def front():
+    """The native torch front end (csrc/front.cpp), loaded on the first call of one of its
+    functions.  Raises if it is not built."""
+    global _front
+    if _front is None:
+        load()
+        if not os.path.exists(_build.FRONT):
+            raise RuntimeError(f"the front end {_build.FRONT} is not built; run python -m "
+                               "causal_attention_fwd_attn_b200.build")
+        _front = importlib.import_module("._front", __package__)
+    return _front
 
 
 def status_string(status: int) -> str:
@@ -275,13 +280,13 @@ def forge_attn_bf16_to_fp16(src, dst, n, overflow, stream):
 
 
 def _ref(value):
-    """What to pass for a structure: its address, or its bytes as they are, or None."""
-    return ctypes.addressof(value) if isinstance(value, ctypes.Structure) else value
+    """Address of a structure (None stays None); the caller keeps the structure alive."""
+    return None if value is None else ctypes.addressof(value)
 
 
 def forge_qkv_fwd(config, q, k, v, q_out, k_out, v_out, flags, stream):
-    """config: a QkvConfig; q, k, v: QkvTensor or None (or the bytes of qkv_config / qkv_tensor);
-    outputs: device addresses or None."""
+    """config: a QkvConfig; q, k, v: QkvTensor or None; outputs: device
+    addresses or None."""
     return load().forge_qkv_fwd(_ref(config), _ref(q), _ref(k), _ref(v), q_out, k_out, v_out, flags,
                                 stream)
 
@@ -292,8 +297,8 @@ def forge_qkv_bwd_workspace_size(d):
 
 def forge_qkv_bwd(config, dq, dk, dv, q, k, q_grad, k_grad, v_grad, dq_weight, dk_weight, accumulate,
                   workspace, workspace_bytes, flags, stream):
-    """config: a QkvConfig; q, k and the *_grad: QkvTensor or None (or their bytes); the rest
-    device addresses."""
+    """config: a QkvConfig; q, k and the *_grad: QkvTensor or None; the rest device
+    addresses."""
     return load().forge_qkv_bwd(_ref(config), dq, dk, dv, _ref(q), _ref(k), _ref(q_grad),
                                 _ref(k_grad), _ref(v_grad), dq_weight, dk_weight, accumulate,
                                 workspace, workspace_bytes, flags, stream)

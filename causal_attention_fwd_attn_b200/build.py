@@ -1,4 +1,5 @@
-"""Builds libforge_attn.so (the CUDA library behind include/forge_attn.h) in-tree.
+"""Builds libforge_attn.so (the CUDA library behind include/) and _front.so (the torch front
+end of the operators around the attention, a CPython module over it) in-tree.
 
     python -m causal_attention_fwd_attn_b200.build [--verbose]
 
@@ -19,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libforge_attn.so")
+FRONT = os.path.join(PKG, "_front.so")
+FRONT_SOURCE = os.path.join(CSRC, "front.cpp")
 SOURCES = ["forge_attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "tc_probe.cu", "forge_attn_noalloc.cu",
            "adamw.cu", "gemm.cu", "convert.cu", "qkv.cu", "gemm_grouped.cu", "grad.cu"]
 HEADERS = ["sm100_ptx.cuh", "sm100_grouped_ptx.cuh", "forge_internal.h"]
@@ -32,18 +35,59 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _headers():
+    return [os.path.join(INCLUDE, h) for h in ("forge_attn.h", "forge_attn_testing.h", "forge_adamw.h",
+                                               "forge_linear.h")]
+
+
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("forge_attn.h", "forge_attn_testing.h", "forge_adamw.h",
-                                                        "forge_linear.h")]
-    return files
+    return files + _headers()
+
+
+def _newer(target, files) -> bool:
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
-        return False
-    t = os.path.getmtime(LIBRARY)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIBRARY, _inputs()) and _newer(FRONT, [FRONT_SOURCE] + _headers())
+
+
+def _build_front(verbose: bool) -> None:
+    """Compiles csrc/front.cpp against the headers of the torch that runs it and links it with
+    the library beside it."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    includes = [os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for p in includes:
+        cmd += ["-isystem", p]
+    cmd += [FRONT_SOURCE, "-o", FRONT + ".tmp", "-L", PKG, "-l:" + os.path.basename(LIBRARY),
+            "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+    _run(cmd, "g++", verbose)
+    os.replace(FRONT + ".tmp", FRONT)
+
+
+def _run(cmd, what, verbose, show=False) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"{what} failed")
+    if show or verbose:
+        sys.stderr.write(res.stderr)
 
 
 def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) -> str:
@@ -56,15 +100,11 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     if ptxas_info:
         cmd += ["-Xptxas", "-v"]
     cmd += [os.path.join(CSRC, s) for s in SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed")
-    if ptxas_info or verbose:
-        sys.stderr.write(res.stderr)
-    os.replace(LIBRARY + ".tmp", LIBRARY)
+    if force or ptxas_info or not _newer(LIBRARY, _inputs()):
+        _run(cmd, "nvcc", verbose, show=ptxas_info)
+        os.replace(LIBRARY + ".tmp", LIBRARY)
+    if force or not _newer(FRONT, [FRONT_SOURCE] + _headers()):
+        _build_front(verbose)
     return LIBRARY
 
 

@@ -3,19 +3,30 @@
 // offsets are read on the device, so that a router's counts never visit the host.
 //   forward   y  = x w_e^T       backward  dx = dy w_e,   dw_e (+)= dy_e^T x_e
 //
+// Both kernels run on pairs of SMs (clusters of two blocks, cta_group::2): a product of
+// 256 x N x 16 in which each block holds half of A's rows and half of B's, so that an
+// operand byte in shared memory feeds twice the work that it does on one SM.  Shared-memory
+// traffic is what paces the one-SM kernels (gemm.cu).
+//
 // Forward and dX are one kernel (grouped_rows_kernel).  It computes the transposed product:
-// the weights' features are the 128 rows of a tile and the expert's tokens its columns, so
+// the weights' features are the 256 rows of a tile and the expert's tokens its columns, so
 // that the ragged dimension is the one whose width a tcgen05 product can vary (any
-// multiple of 16): an expert's rows are cut into equal tiles of at most BN tokens and
+// multiple of 32): an expert's rows are cut into equal tiles of at most BN tokens and
 // each product is as wide as its tile.  Rows of a neighbouring expert that the last copy of
 // a tile brings along only feed columns that are never stored.
 // dW (grouped_dw_kernel) reduces over an expert's tokens, 64 to a step.  In the last step
 // the rows after the expert's end are cleared in shared memory, in both operands (a
 // neighbour's row may hold infinities, which a zero in one operand would not remove).
 //
+// Sums for fp32 outputs: a tensor core cuts the bits off that its accumulator has no room
+// for, an error that points towards zero and grows with the number of additions (2.8e-6
+// relative after 2048 terms, 2e-5 after 16384).  Reductions into fp32 outputs therefore leave
+// tensor memory every 512 terms and go on in registers, rounded to nearest (below 1e-6 at
+// any length).  16-bit outputs round at 2^-9 and more, and take the whole reduction at once.
+//
 // Both are persistent, one block per SM.  Every block reads the offsets into shared
 // memory (each clamped to the rows there are, so that no offsets can lead outside the
-// tensors) and walks the (expert, tile) units in one common order.
+// tensors) and all pairs walk the (expert, tile) units in one common order.
 #include <cmath>
 
 #include "forge_attn.h"
@@ -28,19 +39,27 @@ namespace forge {
 namespace {
 
 constexpr int kMaxExperts = FORGE_LINEAR_MAX_EXPERTS;
-constexpr int kThreads = 192;
-constexpr int kBM = 128, kBK = 64, kBN = 256;
+// Warps: 0 copies, 1 issues the products (in the pair's first block), 2 clears tails (dW),
+// 4..11 the epilogue (tensor memory lanes 32 (w % 4).., half (w - 4) / 4 of the columns).
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kBK = 64;
+constexpr int kHalfM = 128;        // a block's rows of a pair's 256
+constexpr int kAccCols = 256;      // tensor memory columns of one of the two accumulators
+constexpr int kChunkBlocks = 8;    // k-blocks of a reduction's chunk for fp32 outputs
+constexpr int kMaxStages = 10;
 
-enum : uint32_t { kSiteFull = 1, kSiteEmpty, kSiteAccFull, kSiteAccEmpty };
+enum : uint32_t { kSiteFull = 1, kSiteEmpty, kSiteAccFull, kSiteAccEmpty, kSiteLanded };
 
 struct Barriers {
-    uint64_t full[8], empty[8];
+    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t mma_final;
     uint32_t tmem_base;
     int abort;
 };
-static_assert(sizeof(Barriers) <= 256, "barrier block");
+static_assert(sizeof(Barriers) <= 320, "barrier block");
+constexpr int kBarBytes = 320;
 
 // The experts' rows and units: first[e] the first row, unit0[e] the first unit.
 struct Tables {
@@ -53,6 +72,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
                                           volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, site, abort));
 }
+
+// Start of both kernels: barriers, tensor memory, tables; the pair begins together.
+// `full_count`: arrivals that a stage's products wait for.
+template <typename F>
+__device__ __forceinline__ void start(Barriers* bars, Tables* tab, int stages, int full_count,
+                                      const int* offsets, int experts, int rows, F units_of);
 
 // Fills the tables: `units_of(rows)` units to an expert.  Called by the whole block; ends
 // with a barrier.
@@ -84,174 +109,252 @@ __device__ __forceinline__ void fill_tables(Tables* t, const int* offsets, int e
     __syncthreads();
 }
 
-// ------------------------------------------------------------------ forward and dX ----
-constexpr int kRowsStages = 4;
-constexpr int kRowsABytes = kBM * kBK * 2, kRowsBBytes = kBN * kBK * 2;
-constexpr int kRowsStageBytes = kRowsABytes + kRowsBBytes;
-constexpr int kStageRows = 32;  // token rows of one staging buffer of the epilogue
-constexpr int kRowsStagingBytes = kStageRows * kBM * 4;
-constexpr int kRowsOffStaging = kRowsStages * kRowsStageBytes;
-constexpr int kRowsOffTables = kRowsOffStaging + kRowsStagingBytes;
-constexpr int kRowsOffBar = kRowsOffTables + (int)((sizeof(Tables) + 127) / 128 * 128);
-constexpr int kRowsSmem = kRowsOffBar + 256 + 1024;
-static_assert(kRowsSmem <= 232448, "shared memory budget");
-
-struct RowsShape {
-    int rows, experts, features, k_blocks, feature_tiles;
-};
-
-// One unit: features [fm, fm + 128) of expert e for the token rows [r0, r0 + n).
-struct RowsUnit {
-    int e, fm, r0, n;
-};
-__device__ __forceinline__ RowsUnit rows_unit(const Tables* t, const RowsShape& s, int u, int& e) {
-    while (u >= t->unit0[e + 1]) ++e;
-    const int local = u - t->unit0[e], cnt = t->count[e];
-    const int tiles = (cnt + kBN - 1) / kBN;
-    const int f = local / tiles, tn = local - f * tiles;
-    const int width = ((cnt + tiles - 1) / tiles + 15) / 16 * 16;
-    return RowsUnit{e, f * kBM, t->first[e] + tn * width, min(width, cnt - tn * width)};
-}
-
-template <bool W_MN, bool OUT32, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                        const __grid_constant__ CUtensorMap tmap_x,
-                        const int* __restrict__ offsets, void* __restrict__ out, const RowsShape s) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tables* tab = reinterpret_cast<Tables*>(smem + kRowsOffTables);
-    Barriers* bars = reinterpret_cast<Barriers*>(smem + kRowsOffBar);
-    volatile int* abort = &bars->abort;
-    const uint32_t warp = warp_id(), lane = lane_id();
-
+template <typename F>
+__device__ __forceinline__ void start(Barriers* bars, Tables* tab, int stages, int full_count,
+                                      const int* offsets, int experts, int rows, F units_of) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRowsStages; ++i) {
-            mbar_init(&bars->full[i], 1);
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&bars->full[i], full_count);
             mbar_init(&bars->empty[i], 1);
+            mbar_init(&bars->landed[i], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 4);
+            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&bars->mma_final, 1);
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
-        tmem_alloc(&bars->tmem_base, 512);
-        tmem_relinquish();
+    if (warp_id() == 1) {
+        tmem_alloc_pair(&bars->tmem_base, 2 * kAccCols);
+        tmem_relinquish_pair();
     }
-    const int ft = s.feature_tiles;
-    fill_tables(tab, offsets, s.experts, s.rows,
-                [ft](int n) { return (n + kBN - 1) / kBN * ft; });
+    fill_tables(tab, offsets, experts, rows, units_of);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
+}
+
+// End of both kernels: neither block leaves (or gives up tensor memory) while the other may
+// still read or signal it.
+__device__ __forceinline__ void finish(Barriers* bars) {
+    if (warp_id() == 1) mbar_wait_drain(&bars->mma_final, 0);  // all products and signals
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp_id() == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(bars->tmem_base, 2 * kAccCols);
+    }
+}
+
+// ------------------------------------------------------------------ forward and dX ----
+constexpr int kStageRows = 32;  // token rows of one staging buffer of the epilogue
+
+// BN: tokens of a pair's tile.
+template <int BN, bool OUT32>
+struct RowsCfg {
+    static constexpr int kBox = BN / 2;  // token rows a block copies
+    static constexpr int kABytes = kHalfM * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBox * kBK * 2;
+    static constexpr int kRowBytes = kHalfM * (OUT32 ? 4 : 2);
+    static constexpr int kStagingBytes = 2 * kStageRows * kRowBytes;  // one per half
+    static constexpr int kRest =
+        kStagingBytes + (int)((sizeof(Tables) + 127) / 128 * 128) + kBarBytes + 1024;
+    static constexpr int kFit = (232448 - kRest) / kStageBytes;
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int kOffStaging = kStages * kStageBytes;
+    static constexpr int kOffTables = kOffStaging + kStagingBytes;
+    static constexpr int kOffBar = kOffTables + (int)((sizeof(Tables) + 127) / 128 * 128);
+    static constexpr int kSmem = kOffBar + kBarBytes + 1024;
+    static_assert(kSmem <= 232448 && kStages >= 4, "shared memory budget");
+};
+
+struct RowsShape {
+    int rows, experts, features, k_blocks, feature_tiles;
+};
+
+// One unit: features [fm, fm + 256) of expert e for the token rows [r0, r0 + n).
+struct RowsUnit {
+    int e, fm, r0, n;
+};
+template <int BN>
+__device__ __forceinline__ RowsUnit rows_unit(const Tables* t, int u, int& e) {
+    while (u >= t->unit0[e + 1]) ++e;
+    const int local = u - t->unit0[e], cnt = t->count[e];
+    const int tiles = (cnt + BN - 1) / BN;
+    const int f = local / tiles, tn = local - f * tiles;
+    const int width = ((cnt + tiles - 1) / tiles + 31) / 32 * 32;
+    return RowsUnit{e, f * 2 * kHalfM, t->first[e] + tn * width, min(width, cnt - tn * width)};
+}
+__device__ __forceinline__ int round32(int n) { return (n + 31) / 32 * 32; }
+
+template <int BN, bool W_MN, bool OUT32, bool F16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                        const __grid_constant__ CUtensorMap tmap_x,
+                        const int* __restrict__ offsets, void* __restrict__ out, const RowsShape s) {
+    using C = RowsCfg<BN, OUT32>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Tables* tab = reinterpret_cast<Tables*>(smem + C::kOffTables);
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kOffBar);
+    volatile int* abort = &bars->abort;
+    const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int ft = s.feature_tiles;
+    start(bars, tab, C::kStages, 1, offsets, s.experts, s.rows,
+          [ft](int n) { return (n + BN - 1) / BN * ft; });
     const uint32_t tmem = bars->tmem_base;
     const int units = tab->unit0[s.experts];
 
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
+        // Producer.  Both blocks' copies are counted on the first block's barrier.
         if (lane == 0) {
             tma_prefetch_desc(&tmap_w);
             tma_prefetch_desc(&tmap_x);
             int it = 0, e = 0;
-            int last_use[kRowsStages];
-            for (int i = 0; i < kRowsStages; ++i) last_use[i] = -1;
             bool run = true;
-            for (int u = blockIdx.x; run && u < units; u += gridDim.x) {
-                const RowsUnit w = rows_unit(tab, s, u, e);
+            for (int u = pair; run && u < units; u += pairs) {
+                const RowsUnit w = rows_unit<BN>(tab, u, e);
+                const int fm = w.fm + (int)rank * kHalfM, r0 = w.r0 + (int)rank * (round32(w.n) / 2);
                 for (int kb = 0; kb < s.k_blocks; ++kb, ++it) {
-                    const int st = it % kRowsStages, use = it / kRowsStages;
-                    if (use > 0 && !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
+                    const int st = it % C::kStages, use = it / C::kStages;
+                    if (use > 0 &&
+                        !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
                         run = false;
                         break;
                     }
-                    uint8_t* sa = smem + st * kRowsStageBytes;
-                    mbar_arrive_expect_tx(&bars->full[st], kRowsStageBytes);
+                    uint8_t* sa = smem + st * C::kStageBytes;
+                    const uint32_t bar = cluster_addr(&bars->full[st], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * C::kStageBytes);
                     if constexpr (W_MN) {
-                        for (int c = 0; c < kBM / 64; ++c)
-                            tma_load_3d(sa + c * (kBK * 128), &tmap_w, &bars->full[st],
-                                        w.fm + 64 * c, kb * kBK, w.e);
+                        for (int c = 0; c < kHalfM / 64; ++c)
+                            tma_load_3d_pair(sa + c * (kBK * 128), &tmap_w, bar, fm + 64 * c,
+                                             kb * kBK, w.e);
                     } else {
-                        tma_load_3d(sa, &tmap_w, &bars->full[st], kb * kBK, w.fm, w.e);
+                        tma_load_3d_pair(sa, &tmap_w, bar, kb * kBK, fm, w.e);
                     }
-                    tma_load_2d(sa + kRowsABytes, &tmap_x, &bars->full[st], kb * kBK, w.r0);
-                    last_use[st] = use;
+                    tma_load_2d_pair(sa + C::kABytes, &tmap_x, bar, kb * kBK, r0);
                 }
             }
-            if (*abort)
-                for (int i = 0; i < kRowsStages; ++i)
-                    if (last_use[i] >= 0) mbar_wait_drain(&bars->full[i], last_use[i] & 1);
+            if (*abort && rank == 0)  // let copies already issued land before the pair ends
+                for (int k = max(0, it - C::kStages); k < it; ++k)
+                    mbar_wait_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
         }
-    } else if (warp == 1) {
-        // --------------------------------------------------------- MMA issuer
-        constexpr uint32_t kIdesc0 = idesc_f16kind_f32(kBM, 0, W_MN, false, F16);
-        int it = 0, n_unit = 0, e = 0;
+    } else if (warp == 1 && rank == 0) {
+        // MMA issuer.
+        constexpr uint32_t kIdesc0 = idesc_f16kind_f32(2 * kHalfM, 0, W_MN, false, F16);
+        int it = 0, n_acc = 0, e = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++n_unit) {
-            const RowsUnit w = rows_unit(tab, s, u, e);
-            const int buf = n_unit & 1, use = n_unit >> 1;
-            if (use > 0 &&
-                !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t tacc = tmem + buf * kBN;
-            const uint32_t idesc = kIdesc0 | ((uint32_t)((w.n + 15) / 16 * 2) << 17);
-            for (int kb = 0; kb < s.k_blocks; ++kb, ++it) {
-                const int st = it % kRowsStages;
-                if (!warp_wait(&bars->full[st], (it / kRowsStages) & 1, kSiteFull, abort)) {
+        for (int u = pair; ok && u < units; u += pairs) {
+            const RowsUnit w = rows_unit<BN>(tab, u, e);
+            const uint32_t idesc = kIdesc0 | ((uint32_t)(round32(w.n) >> 3) << 17);
+            for (int kb0 = 0; ok && kb0 < s.k_blocks; ++n_acc) {
+                const int kb1 = OUT32 ? min(kb0 + kChunkBlocks, s.k_blocks) : s.k_blocks;
+                const int buf = n_acc & 1, use = n_acc >> 1;
+                if (use > 0 &&
+                    !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t a = smem_u32(smem + st * kRowsStageBytes), b = a + kRowsABytes;
+                const uint32_t tacc = tmem + buf * kAccCols;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int st = it % C::kStages;
+                    if (!warp_wait(&bars->full[st], (it / C::kStages) & 1, kSiteFull, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + st * C::kStageBytes), b = a + C::kABytes;
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk) {
-                    const uint64_t ad = W_MN ? sdesc_sw128(a + kk * 2048, kBK * 128, 1024)
-                                             : sdesc_sw128(a + kk * 32, 16, 1024);
-                    mma_ss_warp(tacc, ad, sdesc_sw128(b + kk * 32, 16, 1024), idesc,
-                                (kb > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        const uint64_t ad = W_MN ? sdesc_sw128(a + kk * 2048, kBK * 128, 1024)
+                                                 : sdesc_sw128(a + kk * 32, 16, 1024);
+                        mma_ss_pair_warp(tacc, ad, sdesc_sw128(b + kk * 32, 16, 1024), idesc,
+                                         (kb > kb0 || kk > 0) ? 1u : 0u);
+                    }
+                    mma_commit_pair_warp(&bars->empty[st]);
                 }
-                mma_commit_warp(&bars->empty[st]);
+                if (ok) mma_commit_pair_warp(&bars->acc_full[buf]);
+                kb0 = kb1;
             }
-            if (ok) mma_commit_warp(&bars->acc_full[buf]);
         }
-        mma_commit_warp(&bars->mma_final);
-        mbar_wait_drain(&bars->mma_final, 0);
-    } else {
-        // ------------------------------------------------------------ epilogue
-        // A thread reads its feature's accumulators 32 tokens at a time; the four warps
-        // turn them into rows of 128 features in shared memory and store those whole.
-        const uint32_t quarter = warp & 3;
+        mma_commit_pair_warp(&bars->mma_final);
+    } else if (warp >= 4) {
+        // Epilogue.  A thread reads its feature's accumulators 32 tokens at a time; the four
+        // warps of a half (the even or the odd 32s) turn them into rows of 128 features in
+        // shared memory and store those whole.
+        const uint32_t quarter = warp & 3, half = (warp >> 2) - 1;
         const uint32_t lane_off = (quarter * 32u) << 16;
-        const int tid = (int)threadIdx.x - 64;
-        constexpr int kEl = OUT32 ? 4 : 2, kRowBytes = kBM * kEl, kChunks = kRowBytes / 16;
-        uint8_t* staging = smem + kRowsOffStaging;
-        int n_unit = 0, e = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++n_unit) {
-            const RowsUnit w = rows_unit(tab, s, u, e);
-            const int buf = n_unit & 1, use = n_unit >> 1;
-            // the four warps go on, or give up, together: they meet at barriers below
-            if (!named_barrier_all(
-                    1, 128, warp_wait(&bars->acc_full[buf], use & 1, kSiteAccFull, abort)))
-                break;
-            tc_fence_after();
+        const int tid = (int)threadIdx.x - 128 * (1 + (int)half);
+        constexpr int kEl = OUT32 ? 4 : 2, kRowBytes = C::kRowBytes, kChunks = kRowBytes / 16;
+        constexpr int kMySteps = (BN / kStageRows + 1) / 2;
+        uint8_t* staging = smem + C::kOffStaging + half * (C::kStagingBytes / 2);
+        const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
+                                       cluster_addr(&bars->acc_empty[1], 0)};
+        int n_acc = 0, e = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += pairs) {
+            const RowsUnit w = rows_unit<BN>(tab, u, e);
+            const int fm = w.fm + (int)rank * kHalfM;
             const int steps = (w.n + kStageRows - 1) / kStageRows;
-            for (int c = 0; c < steps; ++c) {
-                uint32_t r[32];
-                tmem_ld32(tmem + lane_off + buf * kBN + c * kStageRows, r);
-                tmem_wait_ld();
-                if (c == steps - 1) {
+            float sum[OUT32 ? kMySteps * 32 : 1];
+            if constexpr (OUT32) {
+#pragma unroll
+                for (int j = 0; j < kMySteps * 32; ++j) sum[j] = 0.f;
+                const int chunks = (s.k_blocks + kChunkBlocks - 1) / kChunkBlocks;
+                for (int c = 0; ok && c < chunks; ++c, ++n_acc) {
+                    const int buf = n_acc & 1;
+                    ok = named_barrier_all(
+                        1 + half, 128,
+                        warp_wait(&bars->acc_full[buf], (n_acc >> 1) & 1, kSiteAccFull, abort));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < kMySteps; ++q) {
+                        if (2 * q + (int)half >= steps) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+                            tmem_ld16(tmem + lane_off + buf * kAccCols +
+                                          (2 * q + half) * kStageRows + 16 * h, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[32 * q + 16 * h + j] += __uint_as_float(r[j]);
+                        }
+                    }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->acc_empty[buf]);
+                    if (lane == 0) mbar_arrive_at(empty_bar[buf]);
                 }
-                named_barrier_sync(1, 128);  // the staging rows have been read
+                if (!ok) break;
+            } else {
+                ok = named_barrier_all(
+                    1 + half, 128,
+                    warp_wait(&bars->acc_full[n_acc & 1], (n_acc >> 1) & 1, kSiteAccFull, abort));
+                if (!ok) break;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int q = 0; q < kMySteps; ++q) {
+                const int c = 2 * q + (int)half;
+                if (c >= steps) break;
+                uint32_t r[32];
+                if constexpr (OUT32) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[32 * q + j]);
+                } else {
+                    tmem_ld32(tmem + lane_off + (n_acc & 1) * kAccCols + c * kStageRows, r);
+                    tmem_wait_ld();
+                }
+                named_barrier_sync(1 + half, 128);  // the staging rows have been read
 #pragma unroll
                 for (int j = 0; j < kStageRows; ++j) {
                     uint8_t* dst = staging + j * kRowBytes + (quarter * 32 + lane) * kEl;
@@ -260,39 +363,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint16_t*>(dst) =
                             (uint16_t)pack16x2<F16>(__uint_as_float(r[j]), 0.f);
                 }
-                named_barrier_sync(1, 128);
+                named_barrier_sync(1 + half, 128);
                 const int live = min(kStageRows, w.n - c * kStageRows);
                 for (int k = tid; k < live * kChunks; k += 128) {
                     const int row = k / kChunks, col = (k - row * kChunks) * (16 / kEl);
-                    if (w.fm + col >= s.features) continue;
+                    if (fm + col >= s.features) continue;
                     const uint4 v = *reinterpret_cast<const uint4*>(staging + k * 16);
                     const long long off =
-                        (long long)(w.r0 + c * kStageRows + row) * s.features + w.fm + col;
+                        (long long)(w.r0 + c * kStageRows + row) * s.features + fm + col;
                     *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + off * kEl) = v;
                 }
             }
+            if constexpr (!OUT32) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(empty_bar[n_acc & 1]);
+                ++n_acc;
+            }
         }
     }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
+    finish(bars);
 }
 
 // ---------------------------------------------------------------------------- dW ----
+constexpr int kDwHalfBytes = kHalfM * kBK * 2;  // a block's half of either operand
+constexpr int kDwStageBytes = 2 * kDwHalfBytes;
 constexpr int kDwStages = 4;
-constexpr int kDwABytes = kBM * kBK * 2, kDwBBytes = kBN * kBK * 2;
-constexpr int kDwStageBytes = kDwABytes + kDwBBytes;
 constexpr int kDwOffStaging = kDwStages * kDwStageBytes;
 constexpr int kDwBoxBytes = 32 * 128;  // one warp's 32 x 32 fp32 box
-constexpr int kDwOffTables = kDwOffStaging + 4 * kDwBoxBytes;
+constexpr int kDwOffTables = kDwOffStaging + kEpiWarps * 2 * kDwBoxBytes;
 constexpr int kDwOffBar = kDwOffTables + (int)((sizeof(Tables) + 127) / 128 * 128);
-constexpr int kDwSmem = kDwOffBar + 256 + 1024;
-static_assert(kDwSmem <= 232448, "shared memory budget");
+constexpr int kDwSmem = kDwOffBar + kBarBytes + 1024;
+static_assert(kDwSmem <= 232448 && kDwStages <= kMaxStages, "shared memory budget");
 
 struct DwShape {
     int rows, experts, m, n, tiles_m, tiles_n;
@@ -305,22 +407,21 @@ __device__ __forceinline__ DwUnit dw_unit(const Tables* t, const DwShape& s, int
     while (u >= t->unit0[e + 1]) ++e;
     const int local = u - t->unit0[e];
     const int tn = local / s.tiles_m, tm = local - tn * s.tiles_m;
-    return DwUnit{e, tm * kBM, tn * kBN, t->first[e], t->count[e]};
+    return DwUnit{e, tm * 2 * kHalfM, tn * 2 * kHalfM, t->first[e], t->count[e]};
 }
 
 // Clears rows [valid, 64) of the 64-row chunks of a stage (each row is 128 bytes, whatever
 // the swizzle does inside it).
-__device__ __forceinline__ void clear_rows(uint8_t* stage, int chunks, int valid, uint32_t lane) {
+__device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, uint32_t lane) {
     const int per = (kBK - valid) * 8;
-    for (int k = lane; k < chunks * per; k += 32) {
-        const int c = k / per, r = k - c * per;
-        *reinterpret_cast<uint4*>(stage + c * (kBK * 128) + valid * 128 + r * 16) =
-            make_uint4(0, 0, 0, 0);
-    }
+    for (int c = 0; c < kDwStageBytes / (kBK * 128); ++c)
+        for (int r = lane; r < per; r += 32)
+            *reinterpret_cast<uint4*>(stage + c * (kBK * 128) + valid * 128 + r * 16) =
+                make_uint4(0, 0, 0, 0);
 }
 
 template <bool ADD, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_dw_kernel(const __grid_constant__ CUtensorMap tmap_dy,
                       const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_dw,
@@ -331,165 +432,175 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tables* tab = reinterpret_cast<Tables*>(smem + kDwOffTables);
     Barriers* bars = reinterpret_cast<Barriers*>(smem + kDwOffBar);
     volatile int* abort = &bars->abort;
-    const uint32_t warp = warp_id(), lane = lane_id();
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kDwStages; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 4);
-        }
-        mbar_init(&bars->mma_final, 1);
-        bars->abort = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(&bars->tmem_base, 512);
-        tmem_relinquish();
-    }
+    const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // an expert without rows has a zero gradient: written, or nothing to add
     const int per = s.tiles_m * s.tiles_n;
-    fill_tables(tab, offsets, s.experts, s.rows,
-                [per](int n) { return ADD && n == 0 ? 0 : per; });
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    start(bars, tab, kDwStages, 2, offsets, s.experts, s.rows,
+          [per](int n) { return ADD && n == 0 ? 0 : per; });
     const uint32_t tmem = bars->tmem_base;
     const int units = tab->unit0[s.experts];
 
     if (warp == 0) {
+        // Producer.  A block's copies land on its own barrier: warp 2 sees to them first.
         if (lane == 0) {
             tma_prefetch_desc(&tmap_dy);
             tma_prefetch_desc(&tmap_x);
             int it = 0, e = 0;
-            int last_use[kDwStages];
-            for (int i = 0; i < kDwStages; ++i) last_use[i] = -1;
             bool run = true;
-            for (int u = blockIdx.x; run && u < units; u += gridDim.x) {
+            for (int u = pair; run && u < units; u += pairs) {
                 const DwUnit w = dw_unit(tab, s, u, e);
+                const int m0 = w.m0 + (int)rank * kHalfM, n0 = w.n0 + (int)rank * kHalfM;
                 for (int k0 = 0; k0 < w.count; k0 += kBK, ++it) {
                     const int st = it % kDwStages, use = it / kDwStages;
-                    if (use > 0 && !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
+                    if (use > 0 &&
+                        !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
                         run = false;
                         break;
                     }
                     uint8_t* sa = smem + st * kDwStageBytes;
-                    mbar_arrive_expect_tx(&bars->full[st], kDwStageBytes);
-                    for (int c = 0; c < kBM / 64; ++c)
-                        tma_load_2d(sa + c * (kBK * 128), &tmap_dy, &bars->full[st],
-                                    w.m0 + 64 * c, w.r0 + k0);
-                    for (int c = 0; c < kBN / 64; ++c)
-                        tma_load_2d(sa + kDwABytes + c * (kBK * 128), &tmap_x, &bars->full[st],
-                                    w.n0 + 64 * c, w.r0 + k0);
-                    last_use[st] = use;
+                    mbar_arrive_expect_tx(&bars->landed[st], kDwStageBytes);
+                    for (int c = 0; c < kHalfM / 64; ++c) {
+                        tma_load_2d(sa + c * (kBK * 128), &tmap_dy, &bars->landed[st], m0 + 64 * c,
+                                    w.r0 + k0);
+                        tma_load_2d(sa + kDwHalfBytes + c * (kBK * 128), &tmap_x, &bars->landed[st],
+                                    n0 + 64 * c, w.r0 + k0);
+                    }
                 }
             }
-            if (*abort)
-                for (int i = 0; i < kDwStages; ++i)
-                    if (last_use[i] >= 0) mbar_wait_drain(&bars->full[i], last_use[i] & 1);
+            if (*abort)  // let copies already issued land before the block ends
+                for (int k = max(0, it - kDwStages); k < it; ++k)
+                    mbar_wait_drain(&bars->landed[k % kDwStages], (k / kDwStages) & 1);
         }
-    } else if (warp == 1) {
-        constexpr uint32_t kIdesc = idesc_f16kind_f32(kBM, kBN, true, true, F16);
-        int it = 0, n_unit = 0, e = 0;
+    } else if (warp == 2) {
+        // Hands each stage to the pair's products, its tail cleared.
+        const uint32_t full0 = cluster_addr(&bars->full[0], 0);
+        int it = 0, e = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
-            if (w.count == 0) continue;
-            const int buf = n_unit & 1, use = n_unit >> 1;
-            ++n_unit;
-            if (use > 0 &&
-                !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t tacc = tmem + buf * kBN;
             for (int k0 = 0; k0 < w.count; k0 += kBK, ++it) {
                 const int st = it % kDwStages;
-                if (!warp_wait(&bars->full[st], (it / kDwStages) & 1, kSiteFull, abort)) {
+                if (!warp_wait(&bars->landed[st], (it / kDwStages) & 1, kSiteLanded, abort)) {
                     ok = false;
                     break;
                 }
-                uint8_t* stage = smem + st * kDwStageBytes;
                 if (w.count - k0 < kBK) {
-                    clear_rows(stage, (kBM + kBN) / 64, w.count - k0, lane);
+                    clear_rows(smem + st * kDwStageBytes, w.count - k0, lane);
                     fence_proxy_async_smem();
+                    fence_cluster();
                     __syncwarp();
                 }
-                tc_fence_after();
-                const uint32_t a = smem_u32(stage), b = a + kDwABytes;
-#pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_ss_warp(tacc, sdesc_sw128(a + kk * 2048, kBK * 128, 1024),
-                                sdesc_sw128(b + kk * 2048, kBK * 128, 1024), kIdesc,
-                                (k0 > 0 || kk > 0) ? 1u : 0u);
-                mma_commit_warp(&bars->empty[st]);
+                if (lane == 0) mbar_arrive_at(full0 + st * (uint32_t)sizeof(uint64_t));
             }
-            if (ok) mma_commit_warp(&bars->acc_full[buf]);
         }
-        mma_commit_warp(&bars->mma_final);
-        mbar_wait_drain(&bars->mma_final, 0);
-    } else {
-        // A warp stages its 32 rows 32 columns at a time (128-byte swizzle) and one lane
-        // hands the box to the copy engine, which clips it at the expert's last row and
-        // column and, when accumulating, adds it (one addition per element).
-        const uint32_t quarter = warp & 3;
-        const uint32_t lane_off = (quarter * 32u) << 16;
-        uint8_t* box = smem + kDwOffStaging + quarter * kDwBoxBytes;
-        int n_unit = 0, e = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    } else if (warp == 1 && rank == 0) {
+        constexpr uint32_t kIdesc = idesc_f16kind_f32(2 * kHalfM, 2 * kHalfM, true, true, F16);
+        int it = 0, n_acc = 0, e = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
-            const bool empty = w.count == 0;
-            const int buf = n_unit & 1, use = n_unit >> 1;
-            if (!empty) {
-                ++n_unit;
-                if (!warp_wait(&bars->acc_full[buf], use & 1, kSiteAccFull, abort)) break;
-                tc_fence_after();
-            }
-            const int row = w.m0 + (int)quarter * 32;
-            for (int c = 0; c < kBN / 32; ++c) {
-                uint32_t r[32];
-                if (empty) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0;
-                } else {
-                    tmem_ld32(tmem + lane_off + buf * kBN + c * 32, r);
-                    tmem_wait_ld();
-                    if (c == kBN / 32 - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->acc_empty[buf]);
-                    }
+            const int blocks = (w.count + kBK - 1) / kBK;
+            for (int kb0 = 0; ok && kb0 < blocks; kb0 += kChunkBlocks, ++n_acc) {
+                const int kb1 = min(kb0 + kChunkBlocks, blocks);
+                const int buf = n_acc & 1, use = n_acc >> 1;
+                if (use > 0 &&
+                    !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
+                    ok = false;
+                    break;
                 }
-                if (row >= s.m || w.n0 + 32 * c >= s.n) continue;
+                tc_fence_after();
+                const uint32_t tacc = tmem + buf * kAccCols;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int st = it % kDwStages;
+                    if (!warp_wait(&bars->full[st], (it / kDwStages) & 1, kSiteFull, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (w.count - kb * kBK < kBK) fence_cluster();  // rows that were cleared
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + st * kDwStageBytes), b = a + kDwHalfBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_ss_pair_warp(tacc, sdesc_sw128(a + kk * 2048, kBK * 128, 1024),
+                                         sdesc_sw128(b + kk * 2048, kBK * 128, 1024), kIdesc,
+                                         (kb > kb0 || kk > 0) ? 1u : 0u);
+                    mma_commit_pair_warp(&bars->empty[st]);
+                }
+                if (ok) mma_commit_pair_warp(&bars->acc_full[buf]);
+            }
+        }
+        mma_commit_pair_warp(&bars->mma_final);
+    } else if (warp >= 4) {
+        // Epilogue.  A thread adds up its row's 128 columns over the chunks in registers; then
+        // a warp stages its 32 rows in boxes of 32 columns (128-byte swizzle) and one lane
+        // hands them to the copy engine, which clips them at the expert's last row and column
+        // and, when accumulating, adds them (one addition per element).
+        const uint32_t quarter = warp & 3, half = (warp >> 2) - 1;
+        const uint32_t lane_off = (quarter * 32u) << 16;
+        uint8_t* box = smem + kDwOffStaging + (warp - 4) * 2 * kDwBoxBytes;
+        const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
+                                       cluster_addr(&bars->acc_empty[1], 0)};
+        int n_acc = 0, e = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += pairs) {
+            const DwUnit w = dw_unit(tab, s, u, e);
+            const int chunks = (w.count + kChunkBlocks * kBK - 1) / (kChunkBlocks * kBK);
+            float sum[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+            for (int c = 0; c < chunks; ++c, ++n_acc) {
+                const int buf = n_acc & 1;
+                if (!warp_wait(&bars->acc_full[buf], (n_acc >> 1) & 1, kSiteAccFull, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_off + buf * kAccCols + half * 128 + 16 * q, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[16 * q + j] += __uint_as_float(r[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(empty_bar[buf]);
+            }
+            if (!ok) break;
+            const int row = w.m0 + (int)(rank * kHalfM + quarter * 32);
+            const int col = w.n0 + (int)half * 128;
+            if (row >= s.m) continue;
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {  // two boxes to a fence and a wait
+                if (col + 32 * c >= s.n) break;
                 if (lane == 0) tma_store_wait_all_read();
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(box + sw128_offset(lane, j)) =
-                        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float* v = sum + 32 * (c + b) + 4 * j;
+                        *reinterpret_cast<float4*>(box + b * kDwBoxBytes + sw128_offset(lane, j)) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                    }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (ADD) tma_reduce_add_3d(&tmap_dw, box, w.n0 + 32 * c, row, w.e);
-                    else tma_store_3d(&tmap_dw, box, w.n0 + 32 * c, row, w.e);
+                    for (int b = 0; b < 2 && col + 32 * (c + b) < s.n; ++b) {
+                        const uint8_t* src = box + b * kDwBoxBytes;
+                        if constexpr (ADD)
+                            tma_reduce_add_3d(&tmap_dw, src, col + 32 * (c + b), row, w.e);
+                        else tma_store_3d(&tmap_dw, src, col + 32 * (c + b), row, w.e);
+                    }
                     tma_store_commit();
                 }
             }
         }
         if (lane == 0) tma_store_wait_all();
     }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
+    finish(bars);
 }
 
 // ------------------------------------------------------------------------- host ----
@@ -506,18 +617,34 @@ int check_dims(int rows, int experts, int in_f, int out_f) {
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? FORGE_ATTN_OK : FORGE_ATTN_ERR_CUDA; }
 
-template <bool W_MN, bool OUT32, bool F16>
+// Blocks of a launch: two to a pair, as many pairs as there are units or SMs for.
+int grid_of(long long units) {
+    const int pairs = sm_count() / 2;
+    return 2 * (units < 1 ? 1 : (units < pairs ? (int)units : pairs));
+}
+
+template <int BN, bool W_MN, bool OUT32, bool F16>
 cudaError_t launch_rows_t(const CUtensorMap& tw, const CUtensorMap& tx, const int* offsets,
                           void* out, const RowsShape& s, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
-    auto* kernel = grouped_rows_kernel<W_MN, OUT32, F16>;
-    cudaError_t e = set_max_dynamic_smem(kernel, kRowsSmem, configured);
+    auto* kernel = grouped_rows_kernel<BN, W_MN, OUT32, F16>;
+    constexpr int kSmem = RowsCfg<BN, OUT32>::kSmem;
+    cudaError_t e = set_max_dynamic_smem(kernel, kSmem, configured);
     if (e != cudaSuccess) return e;
     // units: at most one partly filled tile to an expert on top of the full ones
-    const long long units = ((long long)s.rows / kBN + s.experts) * s.feature_tiles;
-    const int grid = units < sm_count() ? (int)units : sm_count();
-    kernel<<<grid, kThreads, kRowsSmem, stream>>>(tw, tx, offsets, out, s);
+    const long long units = ((long long)s.rows / BN + s.experts) * s.feature_tiles;
+    kernel<<<grid_of(units), kThreads, kSmem, stream>>>(tw, tx, offsets, out, s);
     return cudaGetLastError();
+}
+
+template <int BN, bool W_MN>
+cudaError_t launch_rows_n(const CUtensorMap& tw, const CUtensorMap& tx, const int* offsets,
+                          void* out, const RowsShape& s, bool f32, bool f16, cudaStream_t cs) {
+    if (f32)
+        return f16 ? launch_rows_t<BN, W_MN, true, true>(tw, tx, offsets, out, s, cs)
+                   : launch_rows_t<BN, W_MN, true, false>(tw, tx, offsets, out, s, cs);
+    return f16 ? launch_rows_t<BN, W_MN, false, true>(tw, tx, offsets, out, s, cs)
+               : launch_rows_t<BN, W_MN, false, false>(tw, tx, offsets, out, s, cs);
 }
 
 template <bool W_MN>
@@ -533,18 +660,22 @@ int launch_rows(const void* x, const void* w, void* out, const int* offsets, int
     if (!aligned16(x) || !aligned16(w) || !aligned16(out)) return FORGE_ATTN_ERR_MISALIGNED;
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0, f32 = (flags & FORGE_ATTN_OUT_F32) != 0;
     const int k = W_MN ? out_f : in_f, features = W_MN ? in_f : out_f;
+    // Tokens of a tile: the host knows the rows but not who has them, so it goes by the
+    // experts' mean.  A tile wider than an expert's rows copies rows that it does not need; a
+    // narrower one reads the expert's weights once for each of its tiles.
+    const int mean = (rows + experts - 1) / experts;
+    const int bn = mean <= 64 ? 64 : (mean <= 128 ? 128 : 256);
     CUtensorMap tw, tx;
-    if (encode_map_3d(&tw, w, in_f, out_f, experts, 64, W_MN ? 64 : kBM, f16 ? kMapF16 : kMapBf16) !=
-            cudaSuccess ||
-        encode_map_2d16(&tx, x, k, rows, 64, kBN, f16) != cudaSuccess)
+    if (encode_map_3d(&tw, w, in_f, out_f, experts, 64, W_MN ? 64 : kHalfM,
+                      f16 ? kMapF16 : kMapBf16) != cudaSuccess ||
+        encode_map_2d16(&tx, x, k, rows, 64, bn / 2, f16) != cudaSuccess)
         return FORGE_ATTN_ERR_CUDA;
-    const RowsShape s{rows, experts, features, (k + kBK - 1) / kBK, (features + kBM - 1) / kBM};
+    const RowsShape s{rows, experts, features, (k + kBK - 1) / kBK,
+                      (features + 2 * kHalfM - 1) / (2 * kHalfM)};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (f32)
-        return status_of(f16 ? launch_rows_t<W_MN, true, true>(tw, tx, offsets, out, s, cs)
-                             : launch_rows_t<W_MN, true, false>(tw, tx, offsets, out, s, cs));
-    return status_of(f16 ? launch_rows_t<W_MN, false, true>(tw, tx, offsets, out, s, cs)
-                         : launch_rows_t<W_MN, false, false>(tw, tx, offsets, out, s, cs));
+    return status_of(bn == 64    ? launch_rows_n<64, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)
+                     : bn == 128 ? launch_rows_n<128, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)
+                                 : launch_rows_n<256, W_MN>(tw, tx, offsets, out, s, f32, f16, cs));
 }
 
 template <bool ADD, bool F16>
@@ -555,8 +686,7 @@ cudaError_t launch_dw_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
     cudaError_t e = set_max_dynamic_smem(kernel, kDwSmem, configured);
     if (e != cudaSuccess) return e;
     const long long units = (long long)s.experts * s.tiles_m * s.tiles_n;
-    const int grid = units < sm_count() ? (int)units : sm_count();
-    kernel<<<grid, kThreads, kDwSmem, stream>>>(ta, tb, td, offsets, s);
+    kernel<<<grid_of(units), kThreads, kDwSmem, stream>>>(ta, tb, td, offsets, s);
     return cudaGetLastError();
 }
 
@@ -610,8 +740,9 @@ int forge_linear_grouped_bwd_dw(const void* dy, const void* x, float* dw, const 
         encode_map_2d16(&tb, x, in_features, rows, 64, kBK, f16) != cudaSuccess ||
         encode_map_3d(&td, dw, in_features, out_features, experts, 32, 32, kMapF32) != cudaSuccess)
         return FORGE_ATTN_ERR_CUDA;
-    const DwShape s{rows, experts, out_features, in_features, (out_features + kBM - 1) / kBM,
-                    (in_features + kBN - 1) / kBN};
+    const DwShape s{rows, experts, out_features, in_features, 
+                    (out_features + 2 * kHalfM - 1) / (2 * kHalfM),
+                    (in_features + 2 * kHalfM - 1) / (2 * kHalfM)};
     if (accumulate)
         return status_of(f16 ? launch_dw_t<true, true>(ta, tb, td, offsets, s, cs)
                              : launch_dw_t<true, false>(ta, tb, td, offsets, s, cs));
