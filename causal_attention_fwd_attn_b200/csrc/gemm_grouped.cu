@@ -130,6 +130,8 @@ __device__ __forceinline__ void start(Barriers* bars, Tables* tab, int stages, i
         tmem_alloc_pair(&bars->tmem_base, 2 * kAccCols);
         tmem_relinquish_pair();
     }
+    allow_dependents_launch();
+    grid_dependency_wait();  // nothing above read or wrote global memory
     fill_tables(tab, offsets, experts, rows, units_of);
     tc_fence_before();
     __syncthreads();
@@ -633,8 +635,8 @@ cudaError_t launch_rows_t(const CUtensorMap& tw, const CUtensorMap& tx, const in
     if (e != cudaSuccess) return e;
     // units: at most one partly filled tile to an expert on top of the full ones
     const long long units = ((long long)s.rows / BN + s.experts) * s.feature_tiles;
-    kernel<<<grid_of(units), kThreads, kSmem, stream>>>(tw, tx, offsets, out, s);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), kSmem, stream, tw, tx, offsets,
+                            out, s);
 }
 
 template <int BN, bool W_MN>
@@ -686,8 +688,8 @@ cudaError_t launch_dw_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
     cudaError_t e = set_max_dynamic_smem(kernel, kDwSmem, configured);
     if (e != cudaSuccess) return e;
     const long long units = (long long)s.experts * s.tiles_m * s.tiles_n;
-    kernel<<<grid_of(units), kThreads, kDwSmem, stream>>>(ta, tb, td, offsets, s);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), kDwSmem, stream, ta, tb, td,
+                            offsets, s);
 }
 
 }  // namespace

@@ -153,6 +153,8 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long e0, lon
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_norm_kernel(const __grid_constant__ Table t, double* __restrict__ partials) {
+    allow_dependents_launch();
+    grid_dependency_wait();
     const int chunks = t.chunk0[t.count];
     double sum = 0.0;
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -177,6 +179,8 @@ __device__ __forceinline__ double norm_of(const double* partials, int n) {
 
 __global__ void __launch_bounds__(kThreads)
     grad_norm_sum_kernel(const double* __restrict__ partials, int n, float* norm_out) {
+    allow_dependents_launch();
+    grid_dependency_wait();
     const double norm = norm_of(partials, n);
     if (threadIdx.x == 0) *norm_out = (float)norm;
 }
@@ -229,6 +233,8 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_clip_kernel(const __grid_constant__ Table t, const double* __restrict__ partials, int n,
                      float max_norm, float* norm_out) {
+    allow_dependents_launch();
+    grid_dependency_wait();
     const double norm = norm_of(partials, n);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
     const float c = norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
@@ -327,17 +333,18 @@ int run(const forge_grad_tensor* tensors, int n_tensors, bool clip, float max_no
             if (n_tensors > kMaxPerLaunch) fill(&t, tensors, first, count, chunk);
             const int grid = grid_for(t);
             if (pass == 0) {
-                grad_norm_kernel<<<grid, kThreads, 0, s>>>(t, partials + parts);
+                e = launch_dependent(grad_norm_kernel, dim3(grid), dim3(kThreads), 0, s, t,
+                                     partials + parts);
                 parts += grid;
             } else {
-                grad_clip_kernel<<<grid, kThreads, 0, s>>>(t, partials, parts, max_norm,
-                                                           first == 0 ? norm_out : nullptr);
+                e = launch_dependent(grad_clip_kernel, dim3(grid), dim3(kThreads), 0, s, t,
+                                     (const double*)partials, parts, max_norm,
+                                     first == 0 ? norm_out : (float*)nullptr);
             }
-            e = cudaGetLastError();
         }
     if (!clip && e == cudaSuccess) {
-        grad_norm_sum_kernel<<<1, kThreads, 0, s>>>(partials, parts, norm_out);
-        e = cudaGetLastError();
+        e = launch_dependent(grad_norm_sum_kernel, dim3(1), dim3(kThreads), 0, s,
+                             (const double*)partials, parts, norm_out);
     }
     return e == cudaSuccess ? FORGE_ATTN_OK : FORGE_ATTN_ERR_CUDA;
 }
