@@ -48,6 +48,7 @@ constexpr int kHalfM = 128;        // a block's rows of a pair's 256
 constexpr int kAccCols = 256;      // tensor memory columns of one of the two accumulators
 constexpr int kChunkBlocks = 8;    // k-blocks of a reduction's chunk for fp32 outputs
 constexpr int kMaxStages = 10;
+constexpr int kMaxSmem = 232448;   // shared memory of a block
 
 enum : uint32_t { kSiteFull = 1, kSiteEmpty, kSiteAccFull, kSiteAccEmpty, kSiteLanded };
 
@@ -61,11 +62,25 @@ struct Barriers {
 static_assert(sizeof(Barriers) <= 320, "barrier block");
 constexpr int kBarBytes = 320;
 
-// The experts' rows and units: first[e] the first row, unit0[e] the first unit.
+// The experts' rows and units: first[e] the first row, unit0[e] the first unit.  In shared
+// memory, after everything else, and no larger than the experts need.
 struct Tables {
-    int first[kMaxExperts + 1];
-    int count[kMaxExperts];
-    int unit0[kMaxExperts + 1];
+    int *first, *count, *unit0;  // [experts + 1] each
+    __device__ Tables(uint8_t* at, int experts)
+        : first(reinterpret_cast<int*>(at)), count(first + experts + 1), unit0(count + experts + 1) {}
+};
+__host__ __device__ constexpr int tables_bytes(int experts) { return 3 * (experts + 1) * 4; }
+
+// A place in the ring of stages.
+struct Ring {
+    int st = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t site,
@@ -76,41 +91,41 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 // Start of both kernels: barriers, tensor memory, tables; the pair begins together.
 // `full_count`: arrivals that a stage's products wait for.
 template <typename F>
-__device__ __forceinline__ void start(Barriers* bars, Tables* tab, int stages, int full_count,
+__device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
                                       const int* offsets, int experts, int rows, F units_of);
 
 // Fills the tables: `units_of(rows)` units to an expert.  Called by the whole block; ends
 // with a barrier.
 template <typename F>
-__device__ __forceinline__ void fill_tables(Tables* t, const int* offsets, int experts, int rows,
+__device__ __forceinline__ void fill_tables(const Tables& t, const int* offsets, int experts, int rows,
                                             F units_of) {
     for (int e = threadIdx.x; e <= experts; e += blockDim.x)
-        t->first[e] = min(max(offsets[e], 0), rows);
+        t.first[e] = min(max(offsets[e], 0), rows);
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += blockDim.x)
-        t->count[e] = max(t->first[e + 1] - t->first[e], 0);
+        t.count[e] = max(t.first[e + 1] - t.first[e], 0);
     __syncthreads();
     if (warp_id() == 0) {
         int base = 0;
         for (int e0 = 0; e0 < experts; e0 += 32) {
             const int e = e0 + (int)lane_id();
-            int u = e < experts ? units_of(t->count[e]) : 0;
+            int u = e < experts ? units_of(t.count[e]) : 0;
             int sum = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int below = __shfl_up_sync(0xffffffffu, sum, o);
                 if ((int)lane_id() >= o) sum += below;
             }
-            if (e < experts) t->unit0[e] = base + sum - u;
+            if (e < experts) t.unit0[e] = base + sum - u;
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (lane_id() == 0) t->unit0[experts] = base;
+        if (lane_id() == 0) t.unit0[experts] = base;
     }
     __syncthreads();
 }
 
 template <typename F>
-__device__ __forceinline__ void start(Barriers* bars, Tables* tab, int stages, int full_count,
+__device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
                                       const int* offsets, int experts, int rows, F units_of) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -164,19 +179,17 @@ struct RowsCfg {
     static constexpr int kStageBytes = kABytes + kBox * kBK * 2;
     static constexpr int kRowBytes = kHalfM * (OUT32 ? 4 : 2);
     static constexpr int kStagingBytes = 2 * kStageRows * kRowBytes;  // one per half
-    static constexpr int kRest =
-        kStagingBytes + (int)((sizeof(Tables) + 127) / 128 * 128) + kBarBytes + 1024;
-    static constexpr int kFit = (232448 - kRest) / kStageBytes;
-    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr int kOffStaging = kStages * kStageBytes;
-    static constexpr int kOffTables = kOffStaging + kStagingBytes;
-    static constexpr int kOffBar = kOffTables + (int)((sizeof(Tables) + 127) / 128 * 128);
-    static constexpr int kSmem = kOffBar + kBarBytes + 1024;
-    static_assert(kSmem <= 232448 && kStages >= 4, "shared memory budget");
+    static constexpr int kRest = kStagingBytes + kBarBytes + 1024;
+    // stages that fit beside the tables of that many experts
+    static constexpr int stages(int experts) {
+        const int fit = (kMaxSmem - kRest - tables_bytes(experts)) / kStageBytes;
+        return fit < kMaxStages ? fit : kMaxStages;
+    }
+    static_assert(stages(kMaxExperts) >= 4, "shared memory budget");
 };
 
 struct RowsShape {
-    int rows, experts, features, k_blocks, feature_tiles;
+    int rows, experts, features, k_blocks, feature_tiles, stages;
 };
 
 // One unit: features [fm, fm + 256) of expert e for the token rows [r0, r0 + n).
@@ -184,13 +197,13 @@ struct RowsUnit {
     int e, fm, r0, n;
 };
 template <int BN>
-__device__ __forceinline__ RowsUnit rows_unit(const Tables* t, int u, int& e) {
-    while (u >= t->unit0[e + 1]) ++e;
-    const int local = u - t->unit0[e], cnt = t->count[e];
+__device__ __forceinline__ RowsUnit rows_unit(const Tables& t, int u, int& e) {
+    while (u >= t.unit0[e + 1]) ++e;
+    const int local = u - t.unit0[e], cnt = t.count[e];
     const int tiles = (cnt + BN - 1) / BN;
     const int f = local / tiles, tn = local - f * tiles;
     const int width = ((cnt + tiles - 1) / tiles + 31) / 32 * 32;
-    return RowsUnit{e, f * 2 * kHalfM, t->first[e] + tn * width, min(width, cnt - tn * width)};
+    return RowsUnit{e, f * 2 * kHalfM, t.first[e] + tn * width, min(width, cnt - tn * width)};
 }
 __device__ __forceinline__ int round32(int n) { return (n + 31) / 32 * 32; }
 
@@ -203,16 +216,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tables* tab = reinterpret_cast<Tables*>(smem + C::kOffTables);
-    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kOffBar);
+    const int stages = s.stages;
+    uint8_t* const staging0 = smem + stages * C::kStageBytes;
+    Barriers* bars = reinterpret_cast<Barriers*>(staging0 + C::kStagingBytes);
+    const Tables tab(reinterpret_cast<uint8_t*>(bars) + kBarBytes, s.experts);
     volatile int* abort = &bars->abort;
     const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int ft = s.feature_tiles;
-    start(bars, tab, C::kStages, 1, offsets, s.experts, s.rows,
+    start(bars, tab, stages, 1, offsets, s.experts, s.rows,
           [ft](int n) { return (n + BN - 1) / BN * ft; });
     const uint32_t tmem = bars->tmem_base;
-    const int units = tab->unit0[s.experts];
+    const int units = tab.unit0[s.experts];
 
     if (warp == 0) {
         // Producer.  Both blocks' copies are counted on the first block's barrier.
@@ -220,14 +235,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tmap_w);
             tma_prefetch_desc(&tmap_x);
             int it = 0, e = 0;
+            Ring at;
             bool run = true;
             for (int u = pair; run && u < units; u += pairs) {
                 const RowsUnit w = rows_unit<BN>(tab, u, e);
                 const int fm = w.fm + (int)rank * kHalfM, r0 = w.r0 + (int)rank * (round32(w.n) / 2);
-                for (int kb = 0; kb < s.k_blocks; ++kb, ++it) {
-                    const int st = it % C::kStages, use = it / C::kStages;
-                    if (use > 0 &&
-                        !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
+                for (int kb = 0; kb < s.k_blocks; ++kb, ++it, at.next(stages)) {
+                    const int st = at.st;
+                    if (it >= stages &&
+                        !mbar_wait(&bars->empty[st], at.phase ^ 1, kSiteEmpty, abort)) {
                         run = false;
                         break;
                     }
@@ -245,13 +261,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (*abort && rank == 0)  // let copies already issued land before the pair ends
-                for (int k = max(0, it - C::kStages); k < it; ++k)
-                    mbar_wait_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
+                for (int k = max(0, it - stages); k < it; ++k)
+                    mbar_wait_drain(&bars->full[k % stages], (k / stages) & 1);
         }
     } else if (warp == 1 && rank == 0) {
         // MMA issuer.
         constexpr uint32_t kIdesc0 = idesc_f16kind_f32(2 * kHalfM, 0, W_MN, false, F16);
-        int it = 0, n_acc = 0, e = 0;
+        Ring at;
+        int n_acc = 0, e = 0;
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
             const RowsUnit w = rows_unit<BN>(tab, u, e);
@@ -266,9 +283,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t tacc = tmem + buf * kAccCols;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % C::kStages;
-                    if (!warp_wait(&bars->full[st], (it / C::kStages) & 1, kSiteFull, abort)) {
+                for (int kb = kb0; kb < kb1; ++kb, at.next(stages)) {
+                    const int st = at.st;
+                    if (!warp_wait(&bars->full[st], at.phase, kSiteFull, abort)) {
                         ok = false;
                         break;
                     }
@@ -297,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int tid = (int)threadIdx.x - 128 * (1 + (int)half);
         constexpr int kEl = OUT32 ? 4 : 2, kRowBytes = C::kRowBytes, kChunks = kRowBytes / 16;
         constexpr int kMySteps = (BN / kStageRows + 1) / 2;
-        uint8_t* staging = smem + C::kOffStaging + half * (C::kStagingBytes / 2);
+        uint8_t* staging = staging0 + half * (C::kStagingBytes / 2);
         const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
                                        cluster_addr(&bars->acc_empty[1], 0)};
         int n_acc = 0, e = 0;
@@ -390,26 +407,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------- dW ----
 constexpr int kDwHalfBytes = kHalfM * kBK * 2;  // a block's half of either operand
 constexpr int kDwStageBytes = 2 * kDwHalfBytes;
-constexpr int kDwStages = 4;
-constexpr int kDwOffStaging = kDwStages * kDwStageBytes;
-constexpr int kDwBoxBytes = 32 * 128;  // one warp's 32 x 32 fp32 box
-constexpr int kDwOffTables = kDwOffStaging + kEpiWarps * 2 * kDwBoxBytes;
-constexpr int kDwOffBar = kDwOffTables + (int)((sizeof(Tables) + 127) / 128 * 128);
-constexpr int kDwSmem = kDwOffBar + kBarBytes + 1024;
-static_assert(kDwSmem <= 232448 && kDwStages <= kMaxStages, "shared memory budget");
+constexpr int kDwBoxBytes = 32 * 128;  // one 32 x 32 fp32 box; two to a warp
+constexpr int kDwStagingBytes = kEpiWarps * 2 * kDwBoxBytes;
+// Five stages beside the tables of up to 143 experts, four beside larger ones (dW of 16384
+// rows, 8 experts, 2048 -> 4096: DW_STAGES).
+constexpr int dw_stages(int experts) {
+    return (kMaxSmem - kDwStagingBytes - kBarBytes - 1024 - tables_bytes(experts)) / kDwStageBytes;
+}
+static_assert(dw_stages(kMaxExperts) >= 4 && dw_stages(1) <= kMaxStages, "shared memory budget");
 
 struct DwShape {
-    int rows, experts, m, n, tiles_m, tiles_n;
+    int rows, experts, m, n, tiles_m, tiles_n, stages;
 };
 
 struct DwUnit {
     int e, m0, n0, r0, count;
 };
-__device__ __forceinline__ DwUnit dw_unit(const Tables* t, const DwShape& s, int u, int& e) {
-    while (u >= t->unit0[e + 1]) ++e;
-    const int local = u - t->unit0[e];
+__device__ __forceinline__ DwUnit dw_unit(const Tables& t, const DwShape& s, int u, int& e) {
+    while (u >= t.unit0[e + 1]) ++e;
+    const int local = u - t.unit0[e];
     const int tn = local / s.tiles_m, tm = local - tn * s.tiles_m;
-    return DwUnit{e, tm * 2 * kHalfM, tn * 2 * kHalfM, t->first[e], t->count[e]};
+    return DwUnit{e, tm * 2 * kHalfM, tn * 2 * kHalfM, t.first[e], t.count[e]};
 }
 
 // Clears rows [valid, 64) of the 64-row chunks of a stage (each row is 128 bytes, whatever
@@ -431,74 +449,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tables* tab = reinterpret_cast<Tables*>(smem + kDwOffTables);
-    Barriers* bars = reinterpret_cast<Barriers*>(smem + kDwOffBar);
+    const int stages = s.stages;
+    uint8_t* const staging0 = smem + stages * kDwStageBytes;
+    Barriers* bars = reinterpret_cast<Barriers*>(staging0 + kDwStagingBytes);
+    const Tables tab(reinterpret_cast<uint8_t*>(bars) + kBarBytes, s.experts);
     volatile int* abort = &bars->abort;
     const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // an expert without rows has a zero gradient: written, or nothing to add
     const int per = s.tiles_m * s.tiles_n;
-    start(bars, tab, kDwStages, 2, offsets, s.experts, s.rows,
+    start(bars, tab, stages, 2, offsets, s.experts, s.rows,
           [per](int n) { return ADD && n == 0 ? 0 : per; });
     const uint32_t tmem = bars->tmem_base;
-    const int units = tab->unit0[s.experts];
+    const int units = tab.unit0[s.experts];
 
     if (warp == 0) {
-        // Producer.  A block's copies land on its own barrier: warp 2 sees to them first.
+        // Producer.  A stage's products wait for both blocks: for the bytes of both on the
+        // first block's barrier, and for an arrival of each.  A tail (less than 64 rows) lands on
+        // its block's own barrier, for warp 2 to clear the rest and arrive.
         if (lane == 0) {
             tma_prefetch_desc(&tmap_dy);
             tma_prefetch_desc(&tmap_x);
             int it = 0, e = 0;
+            Ring at;
+            uint32_t tail_phases = 0;  // of the stages' `landed`
             bool run = true;
             for (int u = pair; run && u < units; u += pairs) {
                 const DwUnit w = dw_unit(tab, s, u, e);
                 const int m0 = w.m0 + (int)rank * kHalfM, n0 = w.n0 + (int)rank * kHalfM;
-                for (int k0 = 0; k0 < w.count; k0 += kBK, ++it) {
-                    const int st = it % kDwStages, use = it / kDwStages;
-                    if (use > 0 &&
-                        !mbar_wait(&bars->empty[st], (use - 1) & 1, kSiteEmpty, abort)) {
+                for (int k0 = 0; k0 < w.count; k0 += kBK, ++it, at.next(stages)) {
+                    const int st = at.st;
+                    if (it >= stages &&
+                        !mbar_wait(&bars->empty[st], at.phase ^ 1, kSiteEmpty, abort)) {
                         run = false;
                         break;
                     }
                     uint8_t* sa = smem + st * kDwStageBytes;
-                    mbar_arrive_expect_tx(&bars->landed[st], kDwStageBytes);
+                    const bool tail = w.count - k0 < kBK;
+                    const uint32_t bar = tail ? smem_u32(&bars->landed[st])
+                                              : cluster_addr(&bars->full[st], 0);
+                    if (tail) tail_phases ^= 1u << st;
+                    mbar_arrive_expect_tx_at(bar, kDwStageBytes);
                     for (int c = 0; c < kHalfM / 64; ++c) {
-                        tma_load_2d(sa + c * (kBK * 128), &tmap_dy, &bars->landed[st], m0 + 64 * c,
-                                    w.r0 + k0);
-                        tma_load_2d(sa + kDwHalfBytes + c * (kBK * 128), &tmap_x, &bars->landed[st],
-                                    n0 + 64 * c, w.r0 + k0);
+                        tma_load_2d_pair(sa + c * (kBK * 128), &tmap_dy, bar, m0 + 64 * c, w.r0 + k0);
+                        tma_load_2d_pair(sa + kDwHalfBytes + c * (kBK * 128), &tmap_x, bar,
+                                         n0 + 64 * c, w.r0 + k0);
                     }
                 }
             }
-            if (*abort)  // let copies already issued land before the block ends
-                for (int k = max(0, it - kDwStages); k < it; ++k)
-                    mbar_wait_drain(&bars->landed[k % kDwStages], (k / kDwStages) & 1);
+            if (*abort)  // let copies already issued land before the pair ends
+                for (int k = max(0, it - stages); k < it; ++k) {
+                    const int st = k % stages;
+                    if (rank == 0) mbar_wait_drain(&bars->full[st], (k / stages) & 1);
+                    mbar_wait_drain(&bars->landed[st], ((tail_phases >> st) & 1) ^ 1);
+                }
         }
     } else if (warp == 2) {
-        // Hands each stage to the pair's products, its tail cleared.
-        const uint32_t full0 = cluster_addr(&bars->full[0], 0);
+        // Clears the tails.
+        uint32_t tail_phases = 0;
         int it = 0, e = 0;
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
-            for (int k0 = 0; k0 < w.count; k0 += kBK, ++it) {
-                const int st = it % kDwStages;
-                if (!warp_wait(&bars->landed[st], (it / kDwStages) & 1, kSiteLanded, abort)) {
-                    ok = false;
-                    break;
-                }
-                if (w.count - k0 < kBK) {
-                    clear_rows(smem + st * kDwStageBytes, w.count - k0, lane);
-                    fence_proxy_async_smem();
-                    fence_cluster();
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive_at(full0 + st * (uint32_t)sizeof(uint64_t));
-            }
+            const int blocks = (w.count + kBK - 1) / kBK, valid = w.count % kBK;
+            it += blocks;
+            if (valid == 0) continue;
+            const int st = (it - 1) % stages;
+            ok = warp_wait(&bars->landed[st], (tail_phases >> st) & 1, kSiteLanded, abort);
+            if (!ok) break;
+            tail_phases ^= 1u << st;
+            clear_rows(smem + st * kDwStageBytes, valid, lane);
+            fence_proxy_async_smem();
+            fence_cluster();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(cluster_addr(&bars->full[st], 0));
         }
     } else if (warp == 1 && rank == 0) {
         constexpr uint32_t kIdesc = idesc_f16kind_f32(2 * kHalfM, 2 * kHalfM, true, true, F16);
-        int it = 0, n_acc = 0, e = 0;
+        Ring at;
+        int n_acc = 0, e = 0;
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
@@ -513,9 +542,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t tacc = tmem + buf * kAccCols;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % kDwStages;
-                    if (!warp_wait(&bars->full[st], (it / kDwStages) & 1, kSiteFull, abort)) {
+                for (int kb = kb0; kb < kb1; ++kb, at.next(stages)) {
+                    const int st = at.st;
+                    if (!warp_wait(&bars->full[st], at.phase, kSiteFull, abort)) {
                         ok = false;
                         break;
                     }
@@ -540,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // and, when accumulating, adds them (one addition per element).
         const uint32_t quarter = warp & 3, half = (warp >> 2) - 1;
         const uint32_t lane_off = (quarter * 32u) << 16;
-        uint8_t* box = smem + kDwOffStaging + (warp - 4) * 2 * kDwBoxBytes;
+        uint8_t* box = staging0 + (warp - 4) * 2 * kDwBoxBytes;
         const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
                                        cluster_addr(&bars->acc_empty[1], 0)};
         int n_acc = 0, e = 0;
@@ -630,13 +659,16 @@ cudaError_t launch_rows_t(const CUtensorMap& tw, const CUtensorMap& tx, const in
                           void* out, const RowsShape& s, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
     auto* kernel = grouped_rows_kernel<BN, W_MN, OUT32, F16>;
-    constexpr int kSmem = RowsCfg<BN, OUT32>::kSmem;
-    cudaError_t e = set_max_dynamic_smem(kernel, kSmem, configured);
+    using C = RowsCfg<BN, OUT32>;
+    cudaError_t e = set_max_dynamic_smem(kernel, kMaxSmem, configured);
     if (e != cudaSuccess) return e;
+    RowsShape shape = s;
+    shape.stages = C::stages(s.experts);
+    const int smem = shape.stages * C::kStageBytes + C::kRest + tables_bytes(s.experts);
     // units: at most one partly filled tile to an expert on top of the full ones
     const long long units = ((long long)s.rows / BN + s.experts) * s.feature_tiles;
-    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), kSmem, stream, tw, tx, offsets,
-                            out, s);
+    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), smem, stream, tw, tx, offsets,
+                            out, shape);
 }
 
 template <int BN, bool W_MN>
@@ -673,7 +705,7 @@ int launch_rows(const void* x, const void* w, void* out, const int* offsets, int
         encode_map_2d16(&tx, x, k, rows, 64, bn / 2, f16) != cudaSuccess)
         return FORGE_ATTN_ERR_CUDA;
     const RowsShape s{rows, experts, features, (k + kBK - 1) / kBK,
-                      (features + 2 * kHalfM - 1) / (2 * kHalfM)};
+                      (features + 2 * kHalfM - 1) / (2 * kHalfM), 0};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return status_of(bn == 64    ? launch_rows_n<64, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)
                      : bn == 128 ? launch_rows_n<128, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)
@@ -685,10 +717,12 @@ cudaError_t launch_dw_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
                         const int* offsets, const DwShape& s, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
     auto* kernel = grouped_dw_kernel<ADD, F16>;
-    cudaError_t e = set_max_dynamic_smem(kernel, kDwSmem, configured);
+    cudaError_t e = set_max_dynamic_smem(kernel, kMaxSmem, configured);
     if (e != cudaSuccess) return e;
+    const int smem = s.stages * kDwStageBytes + kDwStagingBytes + kBarBytes + 1024 +
+                     tables_bytes(s.experts);
     const long long units = (long long)s.experts * s.tiles_m * s.tiles_n;
-    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), kDwSmem, stream, ta, tb, td,
+    return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), smem, stream, ta, tb, td,
                             offsets, s);
 }
 
@@ -744,7 +778,8 @@ int forge_linear_grouped_bwd_dw(const void* dy, const void* x, float* dw, const 
         return FORGE_ATTN_ERR_CUDA;
     const DwShape s{rows, experts, out_features, in_features, 
                     (out_features + 2 * kHalfM - 1) / (2 * kHalfM),
-                    (in_features + 2 * kHalfM - 1) / (2 * kHalfM)};
+                    (in_features + 2 * kHalfM - 1) / (2 * kHalfM),
+                    dw_stages(experts)};
     if (accumulate)
         return status_of(f16 ? launch_dw_t<true, true>(ta, tb, td, offsets, s, cs)
                              : launch_dw_t<true, false>(ta, tb, td, offsets, s, cs));
