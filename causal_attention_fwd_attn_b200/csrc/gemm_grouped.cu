@@ -39,10 +39,10 @@ namespace forge {
 namespace {
 
 constexpr int kMaxExperts = FORGE_LINEAR_MAX_EXPERTS;
-// Warps: 0 copies, 1 issues the products (in the pair's first block), 2 clears tails (dW),
-// 4..11 the epilogue (tensor memory lanes 32 (w % 4).., half (w - 4) / 4 of the columns).
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+// Warps: 0 copies, 1 issues the products (in the pair's first block), 2 clears tails (dW), from
+// 4 on the epilogue, in groups of four (warp w reads tensor memory lanes 32 (w % 4)..).
+constexpr int kGroups = 2;
+constexpr int kThreads = 128 * (1 + kGroups);
 constexpr int kBK = 64;
 constexpr int kHalfM = 128;        // a block's rows of a pair's 256
 constexpr int kAccCols = 256;      // tensor memory columns of one of the two accumulators
@@ -58,6 +58,7 @@ struct Barriers {
     uint64_t mma_final;
     uint32_t tmem_base;
     int abort;
+    int cost[8];  // of the choices of choose_width
 };
 static_assert(sizeof(Barriers) <= 320, "barrier block");
 constexpr int kBarBytes = 320;
@@ -90,21 +91,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 
 // Start of both kernels: barriers, tensor memory, tables; the pair begins together.
 // `full_count`: arrivals that a stage's products wait for.
-template <typename F>
+template <typename G, typename F>
 __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
-                                      const int* offsets, int experts, int rows, F units_of);
+                                      const int* offsets, int experts, int rows, G counted, F units_of);
 
-// Fills the tables: `units_of(rows)` units to an expert.  Called by the whole block; ends
-// with a barrier.
-template <typename F>
+// Fills the tables: `units_of(rows)` units to an expert, asked after `counted()`, which the
+// whole block calls once the rows are known.  Ends with a barrier.
+template <typename G, typename F>
 __device__ __forceinline__ void fill_tables(const Tables& t, const int* offsets, int experts, int rows,
-                                            F units_of) {
+                                            G counted, F units_of) {
     for (int e = threadIdx.x; e <= experts; e += blockDim.x)
         t.first[e] = min(max(offsets[e], 0), rows);
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += blockDim.x)
         t.count[e] = max(t.first[e + 1] - t.first[e], 0);
     __syncthreads();
+    counted();
     if (warp_id() == 0) {
         int base = 0;
         for (int e0 = 0; e0 < experts; e0 += 32) {
@@ -124,9 +126,9 @@ __device__ __forceinline__ void fill_tables(const Tables& t, const int* offsets,
     __syncthreads();
 }
 
-template <typename F>
+template <typename G, typename F>
 __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
-                                      const int* offsets, int experts, int rows, F units_of) {
+                                      const int* offsets, int experts, int rows, G counted, F units_of) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(&bars->full[i], full_count);
@@ -135,7 +137,7 @@ __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int sta
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
+            mbar_init(&bars->acc_empty[b], 2 * 4 * kGroups);
         }
         mbar_init(&bars->mma_final, 1);
         bars->abort = 0;
@@ -147,7 +149,7 @@ __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int sta
     }
     allow_dependents_launch();
     grid_dependency_wait();  // nothing above read or wrote global memory
-    fill_tables(tab, offsets, experts, rows, units_of);
+    fill_tables(tab, offsets, experts, rows, counted, units_of);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -171,46 +173,95 @@ __device__ __forceinline__ void finish(Barriers* bars) {
 // ------------------------------------------------------------------ forward and dX ----
 constexpr int kStageRows = 32;  // token rows of one staging buffer of the epilogue
 
-// BN: tokens of a pair's tile.
+// BN: tokens of a pair's tile at most.
 template <int BN, bool OUT32>
 struct RowsCfg {
-    static constexpr int kBox = BN / 2;  // token rows a block copies
     static constexpr int kABytes = kHalfM * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBox * kBK * 2;
+    static constexpr int kStageBytes = kABytes + BN / 2 * kBK * 2;
     static constexpr int kRowBytes = kHalfM * (OUT32 ? 4 : 2);
-    static constexpr int kStagingBytes = 2 * kStageRows * kRowBytes;  // one per half
+    // 32-token steps of an accumulator that a group of epilogue warps takes
+    static constexpr int kSteps = BN / kStageRows / kGroups;
+    static constexpr int kStagingBytes = kGroups * kStageRows * kRowBytes;
     static constexpr int kRest = kStagingBytes + kBarBytes + 1024;
     // stages that fit beside the tables of that many experts
     static constexpr int stages(int experts) {
         const int fit = (kMaxSmem - kRest - tables_bytes(experts)) / kStageBytes;
         return fit < kMaxStages ? fit : kMaxStages;
     }
-    static_assert(stages(kMaxExperts) >= 4, "shared memory budget");
+    static_assert(stages(kMaxExperts) >= 4 && kSteps >= 1, "shared memory budget");
 };
 
 struct RowsShape {
     int rows, experts, features, k_blocks, feature_tiles, stages;
 };
 
-// One unit: features [fm, fm + 256) of expert e for the token rows [r0, r0 + n).
-struct RowsUnit {
-    int e, fm, r0, n;
+// A token matrix in boxes of 64 x 16 (n + 1): what a block copies of a product 32 (n + 1) wide,
+// no more (the copies are what paces the kernel).
+struct TokenMaps {
+    CUtensorMap box[8];
 };
-template <int BN>
-__device__ __forceinline__ RowsUnit rows_unit(const Tables& t, int u, int& e) {
+
+__device__ __forceinline__ int round32(int n) { return (n + 31) / 32 * 32; }
+
+// An expert's tokens are cut into equal tiles of at most `most`.
+__device__ __forceinline__ int tiles_of(int count, int most) { return (count + most - 1) / most; }
+__device__ __forceinline__ int width_of(int count, int tiles) {
+    return round32((count + tiles - 1) / tiles);
+}
+
+// One unit: features [fm, fm + 256) of expert e for the token rows [r0, r0 + n), products of
+// `width` columns.
+struct RowsUnit {
+    int e, fm, r0, n, width;
+};
+__device__ __forceinline__ RowsUnit rows_unit(const Tables& t, int most, int u, int& e) {
     while (u >= t.unit0[e + 1]) ++e;
     const int local = u - t.unit0[e], cnt = t.count[e];
-    const int tiles = (cnt + BN - 1) / BN;
+    const int tiles = tiles_of(cnt, most);
     const int f = local / tiles, tn = local - f * tiles;
-    const int width = ((cnt + tiles - 1) / tiles + 31) / 32 * 32;
-    return RowsUnit{e, f * 2 * kHalfM, t.first[e] + tn * width, min(width, cnt - tn * width)};
+    const int width = width_of(cnt, tiles);
+    const int n = min(width, cnt - tn * width);
+    return RowsUnit{e, f * 2 * kHalfM, t.first[e] + tn * width, n, round32(n)};
 }
-__device__ __forceinline__ int round32(int n) { return (n + 31) / 32 * 32; }
+
+// The widest tile (BN, or down to BN / 2 in steps of 32) with the least work for the busiest pair:
+// the waves of units times what one costs.  Copies pace the kernel: a row of a k-block takes
+// 256 bytes of weights and one byte for each column, 64 bytes a clock and SM, where the
+// products take two clocks a column.  (Tiles of 512 columns, both accumulators to one tile,
+// copy a third less but cannot overlap their epilogue: forward of 16384 rows, 16 experts,
+// 2048 -> 4096 213 us against 201, not kept.)  A warp weighs each choice; called by the block.
+template <int BN>
+__device__ __forceinline__ int choose_width(const Tables& t, int experts, int feature_tiles,
+                                            int pairs, int* cost) {
+    constexpr int kChoices = BN <= 64 ? 1 : (BN / 64 < 8 ? BN / 64 : 8);
+    if (kChoices == 1) return BN;
+    if ((int)warp_id() < kChoices) {
+        const int most = BN - 32 * (int)warp_id();
+        int units = 0, columns = 0;
+        for (int e = lane_id(); e < experts; e += 32) {
+            const int cnt = t.count[e];
+            if (cnt == 0) continue;
+            const int tiles = tiles_of(cnt, most);
+            units += tiles;
+            columns += tiles * width_of(cnt, tiles);
+        }
+        units = __reduce_add_sync(0xffffffffu, units);
+        columns = __reduce_add_sync(0xffffffffu, columns);
+        const int waves = (int)(((long long)units * feature_tiles + pairs - 1) / pairs);
+        if (lane_id() == 0)
+            cost[warp_id()] = waves * (256 + (units ? columns / units : 0));
+    }
+    __syncthreads();
+    int best = 0;
+    for (int k = 1; k < kChoices; ++k)
+        if (cost[k] < cost[best]) best = k;
+    return BN - 32 * best;
+}
 
 template <int BN, bool W_MN, bool OUT32, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                        const __grid_constant__ CUtensorMap tmap_x,
+                        const __grid_constant__ TokenMaps tmap_x,
                         const int* __restrict__ offsets, void* __restrict__ out, const RowsShape s) {
     using C = RowsCfg<BN, OUT32>;
     extern __shared__ uint8_t smem_raw[];
@@ -224,8 +275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int ft = s.feature_tiles;
+    int most = BN;
     start(bars, tab, stages, 1, offsets, s.experts, s.rows,
-          [ft](int n) { return (n + BN - 1) / BN * ft; });
+          [&] { most = choose_width<BN>(tab, s.experts, ft, pairs, bars->cost); },
+          [&](int n) { return tiles_of(n, most) * ft; });
     const uint32_t tmem = bars->tmem_base;
     const int units = tab.unit0[s.experts];
 
@@ -233,13 +286,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Producer.  Both blocks' copies are counted on the first block's barrier.
         if (lane == 0) {
             tma_prefetch_desc(&tmap_w);
-            tma_prefetch_desc(&tmap_x);
             int it = 0, e = 0;
             Ring at;
             bool run = true;
             for (int u = pair; run && u < units; u += pairs) {
-                const RowsUnit w = rows_unit<BN>(tab, u, e);
-                const int fm = w.fm + (int)rank * kHalfM, r0 = w.r0 + (int)rank * (round32(w.n) / 2);
+                const RowsUnit w = rows_unit(tab, most, u, e);
+                const int fm = w.fm + (int)rank * kHalfM;
+                const int r0 = w.r0 + (int)rank * (w.width / 2);
+                const int bytes = C::kABytes + w.width / 2 * (kBK * 2);
+                const CUtensorMap* box = &tmap_x.box[w.width / 32 - 1];
                 for (int kb = 0; kb < s.k_blocks; ++kb, ++it, at.next(stages)) {
                     const int st = at.st;
                     if (it >= stages &&
@@ -249,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* sa = smem + st * C::kStageBytes;
                     const uint32_t bar = cluster_addr(&bars->full[st], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * C::kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * bytes);
                     if constexpr (W_MN) {
                         for (int c = 0; c < kHalfM / 64; ++c)
                             tma_load_3d_pair(sa + c * (kBK * 128), &tmap_w, bar, fm + 64 * c,
@@ -257,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else {
                         tma_load_3d_pair(sa, &tmap_w, bar, kb * kBK, fm, w.e);
                     }
-                    tma_load_2d_pair(sa + C::kABytes, &tmap_x, bar, kb * kBK, r0);
+                    tma_load_2d_pair(sa + C::kABytes, box, bar, kb * kBK, r0);
                 }
             }
             if (*abort && rank == 0)  // let copies already issued land before the pair ends
@@ -271,8 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int n_acc = 0, e = 0;
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
-            const RowsUnit w = rows_unit<BN>(tab, u, e);
-            const uint32_t idesc = kIdesc0 | ((uint32_t)(round32(w.n) >> 3) << 17);
+            const RowsUnit w = rows_unit(tab, most, u, e);
+            const uint32_t idesc = kIdesc0 | ((uint32_t)(w.width >> 3) << 17);
             for (int kb0 = 0; ok && kb0 < s.k_blocks; ++n_acc) {
                 const int kb1 = OUT32 ? min(kb0 + kChunkBlocks, s.k_blocks) : s.k_blocks;
                 const int buf = n_acc & 1, use = n_acc >> 1;
@@ -306,98 +361,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mma_commit_pair_warp(&bars->mma_final);
     } else if (warp >= 4) {
-        // Epilogue.  A thread reads its feature's accumulators 32 tokens at a time; the four
-        // warps of a half (the even or the odd 32s) turn them into rows of 128 features in
-        // shared memory and store those whole.
-        const uint32_t quarter = warp & 3, half = (warp >> 2) - 1;
+        // Epilogue.  A thread reads its feature's accumulators 32 tokens at a time (a group of
+        // four warps every second 32), hands them back, and turns them into rows of 128
+        // features in shared memory, which the group stores whole.
+        const uint32_t quarter = warp & 3, group = (warp >> 2) - 1;
         const uint32_t lane_off = (quarter * 32u) << 16;
-        const int tid = (int)threadIdx.x - 128 * (1 + (int)half);
+        const int tid = (int)threadIdx.x - 128 * (1 + (int)group);
         constexpr int kEl = OUT32 ? 4 : 2, kRowBytes = C::kRowBytes, kChunks = kRowBytes / 16;
-        constexpr int kMySteps = (BN / kStageRows + 1) / 2;
-        uint8_t* staging = staging0 + half * (C::kStagingBytes / 2);
+        constexpr int kKept = OUT32 ? 32 : 16;  // registers of a step: sums, or 16-bit pairs
+        uint8_t* staging = staging0 + group * (kStageRows * kRowBytes);
         const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
                                        cluster_addr(&bars->acc_empty[1], 0)};
         int n_acc = 0, e = 0;
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
-            const RowsUnit w = rows_unit<BN>(tab, u, e);
+            const RowsUnit w = rows_unit(tab, most, u, e);
             const int fm = w.fm + (int)rank * kHalfM;
-            const int steps = (w.n + kStageRows - 1) / kStageRows;
-            float sum[OUT32 ? kMySteps * 32 : 1];
+            uint32_t kept[C::kSteps][kKept];
             if constexpr (OUT32) {
 #pragma unroll
-                for (int j = 0; j < kMySteps * 32; ++j) sum[j] = 0.f;
-                const int chunks = (s.k_blocks + kChunkBlocks - 1) / kChunkBlocks;
-                for (int c = 0; ok && c < chunks; ++c, ++n_acc) {
-                    const int buf = n_acc & 1;
-                    ok = named_barrier_all(
-                        1 + half, 128,
-                        warp_wait(&bars->acc_full[buf], (n_acc >> 1) & 1, kSiteAccFull, abort));
-                    if (!ok) break;
-                    tc_fence_after();
+                for (int q = 0; q < C::kSteps; ++q)
 #pragma unroll
-                    for (int q = 0; q < kMySteps; ++q) {
-                        if (2 * q + (int)half >= steps) break;
+                    for (int j = 0; j < 32; ++j) kept[q][j] = 0u;
+            }
+            const int chunks = OUT32 ? (s.k_blocks + kChunkBlocks - 1) / kChunkBlocks : 1;
+            for (int c = 0; c < chunks; ++c, ++n_acc) {
+                const int buf = n_acc & 1;
+                // the group goes on, or gives up, together: it meets at barriers below
+                ok = named_barrier_all(
+                    1 + group, 128,
+                    warp_wait(&bars->acc_full[buf], (n_acc >> 1) & 1, kSiteAccFull, abort));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < C::kSteps; ++q) {
+                    const int c0 = (kGroups * q + (int)group) * kStageRows;
+                    if (c0 >= w.width) break;
+                    const uint32_t from = tmem + lane_off + buf * kAccCols + c0;
+                    if constexpr (OUT32) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t r[16];
-                            tmem_ld16(tmem + lane_off + buf * kAccCols +
-                                          (2 * q + half) * kStageRows + 16 * h, r);
+                            tmem_ld16(from + 16 * h, r);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                sum[32 * q + 16 * h + j] += __uint_as_float(r[j]);
+                                kept[q][16 * h + j] =
+                                    __float_as_uint(__uint_as_float(kept[q][16 * h + j]) +
+                                                    __uint_as_float(r[j]));
                         }
+                    } else {
+                        uint32_t r[32];
+                        tmem_ld32(from, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            kept[q][j] = pack16x2<F16>(__uint_as_float(r[2 * j]),
+                                                       __uint_as_float(r[2 * j + 1]));
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(empty_bar[buf]);
                 }
-                if (!ok) break;
-            } else {
-                ok = named_barrier_all(
-                    1 + half, 128,
-                    warp_wait(&bars->acc_full[n_acc & 1], (n_acc >> 1) & 1, kSiteAccFull, abort));
-                if (!ok) break;
-                tc_fence_after();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(empty_bar[buf]);
             }
+            if (!ok) break;
 #pragma unroll
-            for (int q = 0; q < kMySteps; ++q) {
-                const int c = 2 * q + (int)half;
-                if (c >= steps) break;
-                uint32_t r[32];
-                if constexpr (OUT32) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[32 * q + j]);
-                } else {
-                    tmem_ld32(tmem + lane_off + (n_acc & 1) * kAccCols + c * kStageRows, r);
-                    tmem_wait_ld();
-                }
-                named_barrier_sync(1 + half, 128);  // the staging rows have been read
+            for (int q = 0; q < C::kSteps; ++q) {
+                const int c0 = (kGroups * q + (int)group) * kStageRows;
+                if (c0 >= w.width) break;
+                named_barrier_sync(1 + group, 128);  // the staging rows have been read
 #pragma unroll
                 for (int j = 0; j < kStageRows; ++j) {
                     uint8_t* dst = staging + j * kRowBytes + (quarter * 32 + lane) * kEl;
-                    if constexpr (OUT32) *reinterpret_cast<uint32_t*>(dst) = r[j];
+                    if constexpr (OUT32) *reinterpret_cast<uint32_t*>(dst) = kept[q][j];
                     else
                         *reinterpret_cast<uint16_t*>(dst) =
-                            (uint16_t)pack16x2<F16>(__uint_as_float(r[j]), 0.f);
+                            (uint16_t)(kept[q][j / 2] >> (j % 2 * 16));
                 }
-                named_barrier_sync(1 + half, 128);
-                const int live = min(kStageRows, w.n - c * kStageRows);
+                named_barrier_sync(1 + group, 128);
+                const int live = min(kStageRows, w.n - c0);
                 for (int k = tid; k < live * kChunks; k += 128) {
                     const int row = k / kChunks, col = (k - row * kChunks) * (16 / kEl);
                     if (fm + col >= s.features) continue;
                     const uint4 v = *reinterpret_cast<const uint4*>(staging + k * 16);
-                    const long long off =
-                        (long long)(w.r0 + c * kStageRows + row) * s.features + fm + col;
+                    const long long off = (long long)(w.r0 + c0 + row) * s.features + fm + col;
                     *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + off * kEl) = v;
                 }
-            }
-            if constexpr (!OUT32) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(empty_bar[n_acc & 1]);
-                ++n_acc;
             }
         }
     }
@@ -408,9 +457,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kDwHalfBytes = kHalfM * kBK * 2;  // a block's half of either operand
 constexpr int kDwStageBytes = 2 * kDwHalfBytes;
 constexpr int kDwBoxBytes = 32 * 128;  // one 32 x 32 fp32 box; two to a warp
-constexpr int kDwStagingBytes = kEpiWarps * 2 * kDwBoxBytes;
+constexpr int kDwStagingBytes = kGroups * 4 * 2 * kDwBoxBytes;
 // Five stages beside the tables of up to 143 experts, four beside larger ones (dW of 16384
-// rows, 8 experts, 2048 -> 4096: DW_STAGES).
+// rows, 8 experts, 2048 -> 4096: 235 us with five, 240 with four, 262 with three).
 constexpr int dw_stages(int experts) {
     return (kMaxSmem - kDwStagingBytes - kBarBytes - 1024 - tables_bytes(experts)) / kDwStageBytes;
 }
@@ -458,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // an expert without rows has a zero gradient: written, or nothing to add
     const int per = s.tiles_m * s.tiles_n;
-    start(bars, tab, stages, 2, offsets, s.experts, s.rows,
+    start(bars, tab, stages, 2, offsets, s.experts, s.rows, [] {},
           [per](int n) { return ADD && n == 0 ? 0 : per; });
     const uint32_t tmem = bars->tmem_base;
     const int units = tab.unit0[s.experts];
@@ -655,7 +704,7 @@ int grid_of(long long units) {
 }
 
 template <int BN, bool W_MN, bool OUT32, bool F16>
-cudaError_t launch_rows_t(const CUtensorMap& tw, const CUtensorMap& tx, const int* offsets,
+cudaError_t launch_rows_t(const CUtensorMap& tw, const TokenMaps& tx, const int* offsets,
                           void* out, const RowsShape& s, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
     auto* kernel = grouped_rows_kernel<BN, W_MN, OUT32, F16>;
@@ -665,14 +714,15 @@ cudaError_t launch_rows_t(const CUtensorMap& tw, const CUtensorMap& tx, const in
     RowsShape shape = s;
     shape.stages = C::stages(s.experts);
     const int smem = shape.stages * C::kStageBytes + C::kRest + tables_bytes(s.experts);
-    // units: at most one partly filled tile to an expert on top of the full ones
-    const long long units = ((long long)s.rows / BN + s.experts) * s.feature_tiles;
+    // units: at most one partly filled tile to an expert on top of the full ones, with tiles of
+    // BN / 2 and more
+    const long long units = ((long long)s.rows / (BN / 2) + s.experts) * s.feature_tiles;
     return launch_dependent(kernel, dim3(grid_of(units)), dim3(kThreads), smem, stream, tw, tx, offsets,
                             out, shape);
 }
 
 template <int BN, bool W_MN>
-cudaError_t launch_rows_n(const CUtensorMap& tw, const CUtensorMap& tx, const int* offsets,
+cudaError_t launch_rows_n(const CUtensorMap& tw, const TokenMaps& tx, const int* offsets,
                           void* out, const RowsShape& s, bool f32, bool f16, cudaStream_t cs) {
     if (f32)
         return f16 ? launch_rows_t<BN, W_MN, true, true>(tw, tx, offsets, out, s, cs)
@@ -696,16 +746,22 @@ int launch_rows(const void* x, const void* w, void* out, const int* offsets, int
     const int k = W_MN ? out_f : in_f, features = W_MN ? in_f : out_f;
     // Tokens of a tile: the host knows the rows but not who has them, so it goes by the
     // experts' mean.  A tile wider than an expert's rows copies rows that it does not need; a
-    // narrower one reads the expert's weights once for each of its tiles.
-    const int mean = (rows + experts - 1) / experts;
-    const int bn = mean <= 64 ? 64 : (mean <= 128 ? 128 : 256);
-    CUtensorMap tw, tx;
+    // narrower one reads the expert's weights once for each of its tiles.  Where even tiles half
+    // as wide leave pairs of SMs without any, they are halved.
+    const int feature_tiles = (features + 2 * kHalfM - 1) / (2 * kHalfM);
+    const int mean = (rows + experts - 1) / experts, busy = rows < experts ? rows : experts;
+    int bn = mean <= 64 ? 64 : (mean <= 128 ? 128 : 256);
+    while (bn > 64 && (long long)feature_tiles * busy * ((2 * mean + bn - 1) / bn) <= sm_count() / 2)
+        bn /= 2;
+    CUtensorMap tw;
+    TokenMaps tx;
     if (encode_map_3d(&tw, w, in_f, out_f, experts, 64, W_MN ? 64 : kHalfM,
-                      f16 ? kMapF16 : kMapBf16) != cudaSuccess ||
-        encode_map_2d16(&tx, x, k, rows, 64, bn / 2, f16) != cudaSuccess)
+                      f16 ? kMapF16 : kMapBf16) != cudaSuccess)
         return FORGE_ATTN_ERR_CUDA;
-    const RowsShape s{rows, experts, features, (k + kBK - 1) / kBK,
-                      (features + 2 * kHalfM - 1) / (2 * kHalfM), 0};
+    for (int n = 0; n < bn / 32; ++n)
+        if (encode_map_2d16(&tx.box[n], x, k, rows, 64, 16 * (n + 1), f16) != cudaSuccess)
+            return FORGE_ATTN_ERR_CUDA;
+    const RowsShape s{rows, experts, features, (k + kBK - 1) / kBK, feature_tiles, 0};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return status_of(bn == 64    ? launch_rows_n<64, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)
                      : bn == 128 ? launch_rows_n<128, W_MN>(tw, tx, offsets, out, s, f32, f16, cs)

@@ -104,14 +104,16 @@ __device__ __forceinline__ float value(const void* p, long long e) {
 template <int DT>
 constexpr int kPer = DT == FORGE_GRAD_F32 ? 4 : 8;  // values of a 16-byte load
 
-// Sum of squares of elements [e0, e1) over the thread's share of them.
-template <int DT>
+constexpr int kFly = 8;  // 16-byte loads a thread has in flight
+
+// Sum of squares of elements [e0, e1) over the thread's share of them.  KEEP: leave them in L2
+// for the clip pass.
+template <int DT, bool KEEP>
 __device__ __forceinline__ double chunk_squares(const void* g, long long e0, long long e1) {
     constexpr int P = kPer<DT>;
-    constexpr int kFly = 4;  // loads in flight
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(g) + e0 * (16 / P));
     const int n = (int)((e1 - e0) / P);
-    float acc[kFly] = {0.f, 0.f, 0.f, 0.f};
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t any = 0;
     auto take = [&](const uint4& u, float& a) {
         any |= u.x | u.y | u.z | u.w;
@@ -124,9 +126,10 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long e0, lon
     for (; k + (kFly - 1) * kThreads < n; k += kFly * kThreads) {
         uint4 u[kFly];
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) u[j] = __ldg(v + k + j * kThreads);
+        for (int j = 0; j < kFly; ++j)
+            u[j] = KEEP ? __ldg(v + k + j * kThreads) : __ldcs(v + k + j * kThreads);
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) take(u[j], acc[j]);
+        for (int j = 0; j < kFly; ++j) take(u[j], acc[j % 4]);
     }
     for (; k < n; k += kThreads) take(__ldg(v + k), acc[0]);
     float tail = 0.f;
@@ -151,8 +154,16 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long e0, lon
     return s;
 }
 
+template <bool KEEP>
+__device__ __forceinline__ double squares(int dtype, const void* g, long long e0, long long e1) {
+    if (dtype == FORGE_GRAD_F32) return chunk_squares<FORGE_GRAD_F32, KEEP>(g, e0, e1);
+    if (dtype == FORGE_GRAD_BF16) return chunk_squares<FORGE_GRAD_BF16, KEEP>(g, e0, e1);
+    return chunk_squares<FORGE_GRAD_F16, KEEP>(g, e0, e1);
+}
+
+// Chunks from `keep` on stay in L2.
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    grad_norm_kernel(const __grid_constant__ Table t, double* __restrict__ partials) {
+    grad_norm_kernel(const __grid_constant__ Table t, double* __restrict__ partials, int keep) {
     allow_dependents_launch();
     grid_dependency_wait();
     const int chunks = t.chunk0[t.count];
@@ -161,10 +172,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const int i = tensor_of(t, c);
         const long long e0 = (long long)(c - t.chunk0[i]) * t.chunk;
         const long long e1 = min(e0 + t.chunk, t.n[i]);
-        if (t.dtype[i] == FORGE_GRAD_F32) sum += chunk_squares<FORGE_GRAD_F32>(t.grad[i], e0, e1);
-        else if (t.dtype[i] == FORGE_GRAD_BF16)
-            sum += chunk_squares<FORGE_GRAD_BF16>(t.grad[i], e0, e1);
-        else sum += chunk_squares<FORGE_GRAD_F16>(t.grad[i], e0, e1);
+        sum += c >= keep ? squares<true>(t.dtype[i], t.grad[i], e0, e1)
+                         : squares<false>(t.dtype[i], t.grad[i], e0, e1);
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) partials[blockIdx.x] = sum;
@@ -191,7 +200,6 @@ template <int DT>
 __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long e0, long long e1,
                                             float c) {
     constexpr int P = kPer<DT>;
-    constexpr int kFly = 4;
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(g) + e0 * (16 / P));
     uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + e0 * (16 / P));
     const int n = (int)((e1 - e0) / P);
@@ -209,17 +217,17 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long 
             r = make_uint4(pack16x2<F16>(f[0], f[1]), pack16x2<F16>(f[2], f[3]),
                            pack16x2<F16>(f[4], f[5]), pack16x2<F16>(f[6], f[7]));
         }
-        o[k] = r;
+        __stcs(o + k, r);  // (not kept in L2: what the norm pass left there is still needed)
     };
     int k = threadIdx.x;
     for (; k + (kFly - 1) * kThreads < n; k += kFly * kThreads) {
         uint4 u[kFly];
 #pragma unroll
-        for (int j = 0; j < kFly; ++j) u[j] = v[k + j * kThreads];
+        for (int j = 0; j < kFly; ++j) u[j] = __ldcs(v + k + j * kThreads);
 #pragma unroll
         for (int j = 0; j < kFly; ++j) put(k + j * kThreads, u[j]);
     }
-    for (; k < n; k += kThreads) put(k, v[k]);
+    for (; k < n; k += kThreads) put(k, __ldcs(v + k));
     const long long e = e0 + (long long)n * P + threadIdx.x;
     if (e < e1) {
         const float r = value<DT>(g, e) * c;
@@ -271,6 +279,24 @@ int check_tensors(const forge_grad_tensor* tensors, int n_tensors, bool clip) {
         }
     }
     return FORGE_ATTN_OK;
+}
+
+// First chunk of a launch's table whose values are to stay in L2 for the clip pass, which
+// walks the chunks backwards: the last kKeepBytes (of 126 MB of L2).  124.4M fp32 values took
+// 244 us this way, 249 with everything streamed and 251 with everything kept.
+constexpr long long kKeepBytes = 80ll << 20;
+int first_kept(const Table& t) {
+    long long bytes = 0;
+    int c = t.chunk0[t.count];
+    for (int k = t.count - 1; k >= 0 && bytes < kKeepBytes; --k) {
+        const long long chunk = (long long)t.chunk * (t.dtype[k] == FORGE_GRAD_F32 ? 4 : 2);
+        const long long want = (kKeepBytes - bytes + chunk - 1) / chunk;
+        const int n = t.chunk0[k + 1] - t.chunk0[k];
+        const int take = n < want ? n : (int)want;
+        c -= take;
+        bytes += take * chunk;
+    }
+    return c;
 }
 
 // Chunk size of a set: about four chunks to a block, within the limits.
@@ -334,7 +360,7 @@ int run(const forge_grad_tensor* tensors, int n_tensors, bool clip, float max_no
             const int grid = grid_for(t);
             if (pass == 0) {
                 e = launch_dependent(grad_norm_kernel, dim3(grid), dim3(kThreads), 0, s, t,
-                                     partials + parts);
+                                     partials + parts, clip ? first_kept(t) : t.chunk0[t.count]);
                 parts += grid;
             } else {
                 e = launch_dependent(grad_clip_kernel, dim3(grid), dim3(kThreads), 0, s, t,
