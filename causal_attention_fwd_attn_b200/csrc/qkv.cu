@@ -13,7 +13,7 @@
 // Bound by HBM: each value is read once and written once (a shared head is written once
 // for each of its copies).  D / 16 threads hold a head of a token, 16 values each: two
 // 16-byte chunks placed so that both members of every rotated pair are in one thread.
-// A block takes 16 consecutive tokens and a run of heads of q, k or v, computes the tokens'
+// A block takes 16 or 32 consecutive tokens and a run of heads of q, k or v, computes the tokens'
 // sines and cosines once into shared memory, and keeps each thread at its token while it
 // walks the heads.  Angles are reduced in 64 bits (turns =
 // position * f / 2 pi, minus the nearest integer): a 32-bit product would lose the phase
@@ -28,7 +28,7 @@ namespace forge {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTok = 16;  // tokens per block
+constexpr int kSlots = 2;  // heads that a block takes at a time
 
 struct Rope {
     const double* freq;  // [pairs]
@@ -63,7 +63,7 @@ template <int D>
 struct Cfg {
     static constexpr int kLanes = D / 16;              // threads of a head row
     static constexpr int kGroups = kThreads / kLanes;  // rows at a time
-    static constexpr int kSlots = kGroups / kTok;      // heads at a time
+    static constexpr int kTok = kGroups / kSlots;      // tokens of a block: 32 or 16
 };
 
 // First elements of the two 8-element chunks of thread i of a row.  Where whole heads are
@@ -111,11 +111,11 @@ __device__ __forceinline__ void pairs_of(int i, int pairs, int& a, int& b) {
 
 // Tables in shared memory: what thread i of a row reads lies in four 16-byte columns, each
 // with the threads of a row side by side.
-// Angles, [kTok][4][kLanes] of (cos, cos, sin, sin) of two pairs.  A warp takes two tokens.
+// Angles, [kTok][4][kLanes] of (cos, cos, sin, sin) of two pairs.  A warp takes every eighth token.
 template <int D, bool ADJ>
 __device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsigned tok0,
                                             float* cs) {
-    constexpr int L = Cfg<D>::kLanes;
+    constexpr int L = Cfg<D>::kLanes, kTok = Cfg<D>::kTok;
     // The warp's tokens and the lane's pairs at once: the loads, then the long chains of
     // arithmetic, side by side.
     constexpr int N = kTok / (kThreads / 32), M = D / 2 / 32 > 0 ? D / 2 / 32 : 1;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     qkv_fwd_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int nq, int nk,
                    int runs, int per) {
     using C = Cfg<D>;
-    constexpr int L = C::kLanes;
+    constexpr int L = C::kLanes, kTok = C::kTok;
     __shared__ float4 cs[kTok * 4 * L];
     __shared__ float4 wt[4 * L];
     __shared__ uint4 ring[kFwdDepth][2][kThreads];
@@ -269,18 +269,18 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int first = run * per + slot;
     // heads this thread may take, counted from `first` (none where its token is not there)
     const int mine = tok0 + t < s.tokens ? min((run + 1) * per, p.heads) - first : 0;
-    const int rows = (min((run + 1) * per, p.heads) - run * per + C::kSlots - 1) / C::kSlots;
+    const int rows = (min((run + 1) * per, p.heads) - run * per + kSlots - 1) / kSlots;
 
     const uint16_t* x =
         static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st + (mine > 0 ? first * p.sh : 0);
-    const long long x_step = C::kSlots * p.sh;
+    const long long x_step = kSlots * p.sh;
     int fetched = 0;  // heads, in steps of kSlots
     auto prefetch = [&](int at) {
         const bool on = fetched < mine;
         copy16(&ring[at][0][threadIdx.x], x + ea, on);
         copy16(&ring[at][1][threadIdx.x], x + eb, on);
         copies_commit();
-        fetched += C::kSlots;
+        fetched += kSlots;
         if (fetched < mine) x += x_step;  // (past the last row the address stays valid)
     };
 #pragma unroll
@@ -328,12 +328,12 @@ __global__ void __launch_bounds__(kThreads, 3)
             oa = pack8<F16>(f);
             ob = pack8<F16>(f + 4);
         }
-        if (n * C::kSlots < mine) {
+        if (n * kSlots < mine) {
             for (int c = 0; c < p.rep; ++c, y += head) {
                 *reinterpret_cast<uint4*>(y + ea) = oa;
                 *reinterpret_cast<uint4*>(y + eb) = ob;
             }
-            y += (C::kSlots - 1) * p.rep * head;
+            y += (kSlots - 1) * p.rep * head;
         }
         prefetch(n % kFwdDepth);  // into the slots just read
     }
@@ -349,7 +349,6 @@ struct Bwd {
     static constexpr int kRingBytes = kDepth * (kG + 2) * kThreads * 16;
     static constexpr int kBlocksPerSm = G32 ? 2 : 3;  // what shared memory holds
 };
-constexpr int kMaxBwdBlocksPerSm = 3;
 
 // Blocks [0, nq) walk q's (token tile, run of heads) units, the next nk k's, the rest v's.
 // A head row takes p.rep steps, one for each of the attention's heads that share it; the
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
                    int per, float* __restrict__ partials) {
     using C = Cfg<D>;
     using R = Bwd<G32>;
-    constexpr int L = C::kLanes;
+    constexpr int L = C::kLanes, kTok = C::kTok;
     constexpr int kStep = (R::kG + 2) * kThreads;
     extern __shared__ uint4 ring[];  // [kDepth][kG + 2][kThreads]
     __shared__ float4 cs[kTok * 4 * L];
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
     pairs_of<D, ADJ>(i, turn ? rope.pairs : 0, na, nb);
     const float4* my_cs = cs + t * 4 * L + i;
     const long long head = (long long)s.T * D;  // from one of the attention's heads to the next
-    const long long x_step = C::kSlots * p.sh, y_step = C::kSlots * p.gsh;
+    const long long x_step = kSlots * p.sh, y_step = kSlots * p.gsh;
     uint4* const ring0 = ring + threadIdx.x;
 
     for (unsigned unit = blk; unit < units; unit += blocks) {
@@ -412,11 +411,14 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
             pf_at = pf_at == (R::kDepth - 1) * kStep ? 0 : pf_at + kStep;
             const bool on = fetched < mine;
             if constexpr (G32) {
-                const float* src = reinterpret_cast<const float*>(dy);
-                copy16(at, src + ea, on);
-                copy16(at + kThreads, src + ea + 4, on);
-                copy16(at + 2 * kThreads, src + eb, on);
-                copy16(at + 3 * kThreads, src + eb + 4, on);
+                // the row's threads side by side, each 16 bytes: whole sectors, which other
+                // threads of the row will read (a thread's own 32 bytes at a time, every sector
+                // came twice: 90.7 us at B2 T4096 H16 d128)
+                uint4* row = at - i + 3 * (threadIdx.x - i);  // [4 L] of the row's own
+                const float* src = reinterpret_cast<const float*>(dy) + 4 * i;
+                __syncwarp();  // the row's threads have read the slots
+#pragma unroll
+                for (int q = 0; q < 4; ++q) copy16(row + q * L + i, src + q * 4 * L, on);
             } else {
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(dy);
                 copy16(at, src + ea, on);
@@ -429,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
                     copy16(at + (R::kG + 1) * kThreads, x + eb, on);
                 }
                 shared_head = 0;
-                fetched += C::kSlots;
+                fetched += kSlots;
                 if (fetched < mine) {  // (past the last row the addresses stay valid)
-                    dy += ((C::kSlots - 1) * p.rep + 1) * head * (G32 ? 4 : 2);
+                    dy += ((kSlots - 1) * p.rep + 1) * head * (G32 ? 4 : 2);
                     x += x_step;
                 }
             } else if (on) {
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
         }
         __syncthreads();
         int at_now = 0;
-        const int rows = (last - h0 + C::kSlots - 1) / C::kSlots;
+        const int rows = (last - h0 + kSlots - 1) / kSlots;
         for (int row = 0; row < rows; ++row) {
             float2 f[8];
             const uint4* at = ring0 + at_now;
@@ -456,9 +458,11 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
                 at = ring0 + at_now;
                 at_now = at_now == (R::kDepth - 1) * kStep ? 0 : at_now + kStep;
                 if constexpr (G32) {
+                    __syncwarp();  // the row's threads have waited for their copies
+                    const uint4* row = at - i + 3 * (threadIdx.x - i);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint4 v = at[q * kThreads];
+                        const uint4 v = row[(q < 2 ? ea / 4 + q : eb / 4 + q - 2)];
                         a[2 * q] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
                         a[2 * q + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
                     }
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
                     f[j] = fmul2(ffma2(n, both(-m), u[j]), both(r));
                 }
             }
-            if (row * C::kSlots < mine) {
+            if (row * kSlots < mine) {
                 *reinterpret_cast<uint4*>(y + ea) = pack8<F16>(f);
                 *reinterpret_cast<uint4*>(y + eb) = pack8<F16>(f + 4);
                 y += y_step;
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
 
 // dw (+)= sum of the blocks' partials, in 64 bits and in a fixed order.  Block x: eight
 // elements; block y: q or k (partials [first, first + n)).
-constexpr int kSumRows = 32;
+constexpr int kSumRows = 128;
 __global__ void __launch_bounds__(8 * kSumRows)
     qkv_dw_kernel(const float* __restrict__ partials, float* dwq, float* dwk, int nq, int nk, int D,
                   int accumulate) {
@@ -553,12 +557,21 @@ __global__ void __launch_bounds__(8 * kSumRows)
     const int e = blockIdx.x * 8 + col;
     double sum = 0.0;
     for (int k = row; k < n; k += kSumRows) sum += (double)partials[(long long)(first + k) * D + e];
-    __shared__ double red[kSumRows][8];
-    red[row][col] = sum;
+    // rows of a warp, then of the warps
+    constexpr int kWarps = 8 * kSumRows / 32;
+    __shared__ double red[kWarps][8];
+    auto over_rows = [](double v) {
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        return v + __shfl_xor_sync(0xffffffffu, v, 16);
+    };
+    sum = over_rows(sum);
+    if (lane_id() < 8) red[warp_id()][col] = sum;
     __syncthreads();
-    if (row == 0) {
-        for (int k = 1; k < kSumRows; ++k) sum += red[k][col];
-        out[e] = accumulate ? (float)((double)out[e] + sum) : (float)sum;
+    if (warp_id() == 0) {
+        sum = 0.0;
+        for (int w = lane_id() / 8; w < kWarps; w += 4) sum += red[w][col];
+        sum = over_rows(sum);
+        if (lane_id() < 8) out[e] = accumulate ? (float)((double)out[e] + sum) : (float)sum;
     }
 }
 
@@ -639,48 +652,63 @@ Part make_part(const forge_qkv_tensor* x, const float* w, int heads, int rep) {
     return p;
 }
 
-// Blocks of the backward: as many as are resident, shared out among q, k and v by the bytes
-// each moves, at least one to a part that is there and no more than it has units.
+// Blocks of the backward and the heads of a unit's run.  A unit costs kStart (its latencies
+// and its angles) and its rows, in the time of one row of eight to a thread or fewer: the choice
+// is the one with the least work for a resident block plus one unit, the wait for the last.  A block
+// has one unit while that keeps the partial sums of the weights' gradients few.
 struct Blocks {
-    int n[3];
+    int n[3], per;
 };
-Blocks share_out(const double* bytes, const long long* units, int all) {
-    const double sum = bytes[0] + bytes[1] + bytes[2];
-    Blocks r;
-    for (int j = 0; j < 3; ++j) {
-        long long n = units[j] ? (long long)(all * bytes[j] / sum) : 0;
-        if (units[j] && n < 1) n = 1;
-        r.n[j] = (int)(n < units[j] ? n : units[j]);
+constexpr double kStart = 3.0;
+constexpr int kMaxPartials = 1024;  // of q, and of k
+Blocks share_out(const double* row_cost, const int* heads, long long tiles, int resident) {
+    Blocks best{};
+    double best_time = 0.0;
+    for (int rows = 8; rows >= 1; rows /= 2) {
+        Blocks b{};
+        b.per = rows * kSlots;
+        double sum = 0.0, most = 0.0;
+        for (int j = 0; j < 3; ++j) {
+            if (row_cost[j] <= 0.0) continue;
+            const long long units = tiles * ((heads[j] + b.per - 1) / b.per);
+            const int used = heads[j] < b.per ? (heads[j] + kSlots - 1) / kSlots : rows;
+            const double cost = kStart + used * row_cost[j];
+            sum += units * cost;
+            most = cost > most ? cost : most;
+            b.n[j] = (int)(units < kMaxPartials ? units : kMaxPartials);
+        }
+        const double time = sum / resident + most;
+        if (rows == 8 || time < best_time) {
+            best = b;
+            best_time = time;
+        }
     }
-    return r;
+    return best;
 }
 
 // Heads of a block's run: eight rows to a thread, fewer (down to one) where that would leave
 // less than `want` blocks.
-int heads_to_a_block(int d, int heads, long long tiles, long long want) {
-    const int slots = d == 64 ? Cfg<64>::kSlots : Cfg<128>::kSlots;
+int heads_to_a_block(int heads, long long tiles, long long want) {
     int rows = 8;
-    while (rows > 1 && tiles * ((heads + rows * slots - 1) / (rows * slots)) < want) rows /= 2;
-    return rows * slots;
+    while (rows > 1 && tiles * ((heads + rows * kSlots - 1) / (rows * kSlots)) < want) rows /= 2;
+    return rows * kSlots;
 }
-
-int max_bwd_blocks() { return kMaxBwdBlocksPerSm * sm_count() + 3; }
 
 template <int D, bool F16, bool G32, bool ADJ>
 cudaError_t launch_bwd_t(const Parts& parts, const Rope& rope, const Shape& s, const Blocks& n,
-                         int per, float* ws, cudaStream_t stream) {
+                         float* ws, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
     auto* kernel = qkv_bwd_kernel<D, F16, G32, ADJ>;
     cudaError_t e = set_max_dynamic_smem(kernel, Bwd<G32>::kRingBytes, configured);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(n.n[0] + n.n[1] + n.n[2]), dim3(kThreads),
-                            Bwd<G32>::kRingBytes, stream, parts, rope, s, n.n[0], n.n[1], per, ws);
+                            Bwd<G32>::kRingBytes, stream, parts, rope, s, n.n[0], n.n[1], n.per, ws);
 }
 template <int D, bool F16, bool G32>
 cudaError_t launch_bwd(bool adj, const Parts& parts, const Rope& rope, const Shape& s,
-                       const Blocks& n, int per, float* ws, cudaStream_t stream) {
-    return adj ? launch_bwd_t<D, F16, G32, true>(parts, rope, s, n, per, ws, stream)
-               : launch_bwd_t<D, F16, G32, false>(parts, rope, s, n, per, ws, stream);
+                       const Blocks& n, float* ws, cudaStream_t stream) {
+    return adj ? launch_bwd_t<D, F16, G32, true>(parts, rope, s, n, ws, stream)
+               : launch_bwd_t<D, F16, G32, false>(parts, rope, s, n, ws, stream);
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? FORGE_ATTN_OK : FORGE_ATTN_ERR_CUDA; }
@@ -708,11 +736,12 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
         if ((st = check_strides(*in[j], c->B, c->T, heads[j])) != FORGE_ATTN_OK) return st;
         if (!aligned(out[j], 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
-    const long long tokens = (long long)c->B * c->T, tiles = (tokens + kTok - 1) / kTok;
+    const long long tokens = (long long)c->B * c->T, tok = c->d == 64 ? Cfg<64>::kTok : Cfg<128>::kTok,
+                    tiles = (tokens + tok - 1) / tok;
     Parts parts;
     int all = 0, n[3];
     for (int j = 0; j < 3; ++j) all += in[j] ? heads[j] : 0;
-    const int per = heads_to_a_block(c->d, all, tiles, 4LL * sm_count());
+    const int per = heads_to_a_block(all, tiles, 4LL * sm_count());
     for (int j = 0; j < 3; ++j) {
         parts.part[j] = make_part(in[j], weight[j], heads[j], c->H / heads[j]);
         parts.part[j].y = out[j];
@@ -737,7 +766,7 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
 
 size_t forge_qkv_bwd_workspace_size(int d) {
     if (d != 64 && d != 128) return 0;
-    return (size_t)max_bwd_blocks() * d * sizeof(float);
+    return (size_t)(2 * kMaxPartials) * d * sizeof(float);
 }
 
 int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, const void* dv,
@@ -775,16 +804,15 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
         if (!aligned(workspace, 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0, g32 = (flags & FORGE_QKV_GRAD_F32) != 0;
-    const long long tokens = (long long)c->B * c->T, tiles = (tokens + kTok - 1) / kTok;
+    const long long tokens = (long long)c->B * c->T, tok = c->d == 64 ? Cfg<64>::kTok : Cfg<128>::kTok,
+                    tiles = (tokens + tok - 1) / tok;
     const Shape s{c->T, c->H, (unsigned)tokens, c->eps};
     const Rope rope = make_rope(*c);
     const bool adj = (flags & FORGE_QKV_ADJACENT) != 0;
     const int resident = (g32 ? Bwd<true>::kBlocksPerSm : Bwd<false>::kBlocksPerSm) * sm_count();
-    const int per = heads_to_a_block(c->d, c->H, tiles, resident);
     Parts parts;
     Part* p = parts.part;
-    double bytes[3];
-    long long units[3];
+    double row_cost[3];
     for (int j = 0; j < 3; ++j) {
         const bool norm = out[j] && weight[j];
         p[j] = make_part(norm ? x[j] : nullptr, norm ? weight[j] : nullptr, heads[j],
@@ -796,18 +824,18 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
             p[j].gst = out[j]->stride_t;
             p[j].gsh = out[j]->stride_h;
         }
-        units[j] = out[j] ? tiles * ((heads[j] + per - 1) / per) : 0;
-        bytes[j] = out[j] ? (double)c->H * (g32 ? 4 : 2) + heads[j] * (norm ? 4.0 : 2.0) : 0.0;
+        row_cost[j] = out[j] ? 0.5 * p[j].rep + (norm ? 0.5 : 0.0) : 0.0;
     }
-    const Blocks n = share_out(bytes, units, resident);
+    const Blocks n =
+        share_out(row_cost, heads, tiles, resident);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     float* ws = static_cast<float*>(workspace);
 #define FORGE_QKV_BWD(D_)                                                                \
     (c->d != D_   ? cudaErrorInvalidValue                                                \
-     : f16 && g32 ? launch_bwd<D_, true, true>(adj, parts, rope, s, n, per, ws, cs)      \
-     : f16        ? launch_bwd<D_, true, false>(adj, parts, rope, s, n, per, ws, cs)     \
-     : g32        ? launch_bwd<D_, false, true>(adj, parts, rope, s, n, per, ws, cs)     \
-                  : launch_bwd<D_, false, false>(adj, parts, rope, s, n, per, ws, cs))
+     : f16 && g32 ? launch_bwd<D_, true, true>(adj, parts, rope, s, n, ws, cs)      \
+     : f16        ? launch_bwd<D_, true, false>(adj, parts, rope, s, n, ws, cs)     \
+     : g32        ? launch_bwd<D_, false, true>(adj, parts, rope, s, n, ws, cs)     \
+                  : launch_bwd<D_, false, false>(adj, parts, rope, s, n, ws, cs))
     cudaError_t e = c->d == 64 ? FORGE_QKV_BWD(64) : FORGE_QKV_BWD(128);
 #undef FORGE_QKV_BWD
     if (e == cudaSuccess && any_norm)
