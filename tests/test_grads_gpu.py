@@ -65,6 +65,11 @@ def test_sets(sizes, kinds, in_place):
         check(grads, (0.3 if clipped else 3.0) * full + 1e-30, in_place)
 
 
+def test_nothing_at_all():
+    empty = [torch.zeros(0, device=DEV), torch.zeros((0, 5), dtype=torch.bfloat16, device=DEV)]
+    assert fa.grad_norm(empty).item() == 0.0 and fa.grad_clip(empty, 1.0).item() == 0.0
+
+
 def test_nothing_to_clip_leaves_every_bit():
     grads = make([70001, 13], KINDS, 3)
     before = [t.clone() for t in grads]

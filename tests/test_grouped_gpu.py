@@ -155,6 +155,54 @@ def test_several_units_to_a_block():
     run([900, 1300, 20, 777], 264, 2056, seed=21)
 
 
+def test_long_reductions_keep_fp32s_precision():
+    """Chunks of 512 terms leave the tensor cores for sums rounded to nearest: 32 truncations of at
+    most 2^-23 each, half of it on average and all towards zero, on partial sums that grow
+    like sqrt(k) to the chunk's: 32 x 2^-24 x 2/3 = 1.3e-6 at most, however long the sum."""
+    rows, fin, fout = 9000, 264, 136
+    x, dy, w = gen((rows, fin), 1), gen((rows, fout), 2), gen((1, 1032, 8192), 3)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    dw = fa.linear_grouped_bwd_dw(dy.to(DEV), x.to(DEV), off).double().cpu()
+    ref = dy.double().T @ x.double()
+    assert float((dw[0] - ref).norm() / ref.norm()) <= 1.3e-6
+    a = gen((40, 8192), 4)
+    off = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    y = fa.linear_grouped_fwd(a.to(DEV), w.to(DEV), off, out_dtype=torch.float32).double().cpu()
+    ref = a.double() @ w[0].double().T
+    assert float((y - ref).norm() / ref.norm()) <= 1.3e-6
+
+
+@pytest.mark.parametrize("rows", [130, 160, 190, 225, 250, 290, 330, 1000])
+def test_every_tile_width(rows):
+    """One expert: the device's choice of the tile's width goes through its range."""
+    run([rows], 72, 1032, seed=rows, what=("y", "dx"))
+    run([rows] * 20, 64, 264, seed=rows + 1, what=("y",))
+
+
+def test_two_calls_at_once():
+    """Products on two streams at a time, and attention beside them, give what each gives
+    alone."""
+    counts = [300, 0, 129, 33]
+    off = offsets_of(counts).to(DEV)
+    x, dy, w = gen((462, 136), 1).to(DEV), gen((462, 200), 2).to(DEV), gen((4, 200, 136), 3).to(DEV)
+    q = gen((1, 4, 300, 64), 5).to(DEV)
+    want = (fa.linear_grouped_fwd(x, w, off), fa.linear_grouped_bwd_dw(dy, x, off),
+            fa.attn_fwd(q, q, q)[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], [], []]
+    for _ in range(10):
+        for s, call, res in zip(streams, (lambda: fa.linear_grouped_fwd(x, w, off),
+                                          lambda: fa.linear_grouped_bwd_dw(dy, x, off),
+                                          lambda: fa.attn_fwd(q, q, q)[0]), got):
+            with torch.cuda.stream(s):
+                res.append(call())
+    torch.cuda.synchronize()
+    for w_, res in zip(want, got):
+        assert all(torch.equal(w_, r) for r in res)
+    fa.check_device_error()
+
+
 def test_wild_offsets_stay_inside_the_tensors():
     """Offsets past the rows, negative or decreasing are clamped: the calls end, and no row or
     gradient outside the tensors is touched."""

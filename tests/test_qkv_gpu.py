@@ -295,6 +295,36 @@ def test_parts_may_be_left_out():
     assert torch.equal(back, x)
 
 
+def test_one_graph_beside_eager_calls_of_the_same_tensors():
+    """A captured backward shares nothing with eager calls: they may alternate."""
+    case = CASES[3]
+    g, q, k, v, wq, wk, kw, _ = make(case, 29)
+    grads = [torch.randn((2, 6, 130, 64), generator=g).to(DEV) for _ in range(3)]
+    want = fa.qkv_bwd(*grads, q, k, wq, wk, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.qkv_bwd(*grads, q, k, wq, wk, **kw)
+    for _ in range(3):
+        graph.replay()
+        eager = fa.qkv_bwd(*grads, q, k, wq, wk, **kw)
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, eager):
+            assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_more_units_than_partial_sums():
+    """Enough tokens that the backward's blocks take several units each."""
+    B, T, H, d = 1, 40000, 1, 64
+    x = torch.randn((B, T, H, d), device=DEV).to(torch.bfloat16)
+    g = torch.randn((B, H, T, d), device=DEV)
+    w = torch.ones(d, device=DEV)
+    gq, _, _, gw, _ = fa.qkv_bwd(g, g, g, x, x, w, w, eps=EPS)
+    ref, ref_w = oq.head_bwd(f64(g), f64(x), f64(w), None, False, EPS)
+    bound = 1e-5 * np.abs(f64(g).transpose(0, 2, 1, 3) * f64(x)).sum((0, 1, 2)) * 1.5
+    assert (np.abs(f64(gw) - ref_w) <= bound).all()
+    assert np.abs(f64(gq) - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 1e-4
+
+
 def test_front_end_refusals_on_cuda_tensors():
     x = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16, device=DEV)
     freq = torch.ones(32, dtype=torch.float64, device=DEV)
