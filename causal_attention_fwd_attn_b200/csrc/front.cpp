@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -321,11 +322,12 @@ PyObject* qkv_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 }
             }
             PyObject* kept[2] = {Py_None, Py_None};
+            std::unique_ptr<Items> items;  // holds what `kept` points to
             if (given(a[13])) {
-                const Items items(a[13], "weight_out must be (q_weight, k_weight)");
-                if (items.size() != 2) refuse("weight_out must be (q_weight, k_weight)");
-                kept[0] = items[0];
-                kept[1] = items[1];
+                items = std::make_unique<Items>(a[13], "weight_out must be (q_weight, k_weight)");
+                if (items->size() != 2) refuse("weight_out must be (q_weight, k_weight)");
+                kept[0] = (*items)[0];
+                kept[1] = (*items)[1];
             }
             const at::IntArrayRef head(&s.d, 1);
             const float* weights[2] = {s.config.q_weight, s.config.k_weight};
@@ -503,12 +505,13 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             table[k] = forge_grad_tensor{t.data_ptr(), t.data_ptr(), t.numel(),
                                          code_of(t.scalar_type())};
         }
+        std::unique_ptr<Items> out;  // holds the outputs until the launch
         if (clip && given(a[3])) {
-            const Items out(a[3], "outputs must be a sequence of tensors");
-            if (out.size() != n)
-                refuse(std::to_string(n) + " gradients, " + std::to_string(out.size()) + " outputs");
+            out = std::make_unique<Items>(a[3], "outputs must be a sequence of tensors");
+            if (out->size() != n)
+                refuse(std::to_string(n) + " gradients, " + std::to_string(out->size()) + " outputs");
             for (Py_ssize_t k = 0; k < n; ++k) {
-                const Tensor& t = flat(out[k], index, "outputs");
+                const Tensor& t = flat((*out)[k], index, "outputs");
                 if (t.numel() != table[k].n || code_of(t.scalar_type()) != table[k].dtype)
                     refuse("outputs must have their gradients' sizes and types");
                 table[k].out = t.data_ptr();

@@ -223,9 +223,7 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Copies go through a ring in shared memory, each thread's own 16-byte slots: kDepth rows
-// are in flight without a register or a barrier spent on them.  (With the rows in registers
-// instead, two blocks fitted on an SM and the forward at B1 T8000 H32 d128 took 104.5 us.)
-// Where there is no row (on = false) the slot gets zeros and nothing is read.
+// are in flight without a register or a barrier spent on them.  Where there is no row (on = false) the slot gets zeros and nothing is read.
 __device__ __forceinline__ void copy16(uint4* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
                  "r"(on ? 16 : 0)
@@ -241,6 +239,12 @@ __device__ __forceinline__ void copies_wait() {
 
 constexpr int kFwdDepth = 4;
 
+// Forward.  HBM is the bound of large calls: B1 T8000 H32 d128 (393 MB) takes 64.7 us, 6.08 TB/s or
+// 0.93 of the copy rate; loads, arithmetic and stores in one thread without the ring, and
+// scalar fp32 arithmetic, took 104.5.  Smaller ones wait for their chains (positions, angles,
+// rows): B8 T1024 H12 d64 (75 MB) 17.7 us, where a plain copy of as many bytes takes 13.1; 48 tokens of
+// a decoding step 3.7 us, a launch.  Blocks come and go (a persistent form with the next unit's
+// rows and angles under way spent more on keeping its place: 79 us at the first size).
 // Runs of heads that the blocks of a token tile take: nq runs of q's heads, nk of k's and the
 // rest of v's, `per` heads to a run.
 template <int D, bool F16, bool ADJ>
@@ -350,6 +354,11 @@ struct Bwd {
     static constexpr int kBlocksPerSm = G32 ? 2 : 3;  // what shared memory holds
 };
 
+// Backward.  B2 T4096 H16 d128 (268 MB) takes 49 us, 5.4 TB/s or 0.83 of the copy rate, with fp32
+// gradients (369 MB) 63 us, 0.89 of it; B3 T1023 H12 Hkv4 d64 with fp32 gradients (42 MB) 15 us, most of
+// it latencies.  The norm's arithmetic keeps a third of the issue slots busy, so angles and
+// weights are read from shared memory and three blocks fit on an SM (in registers, with two
+// blocks: 62 us at the first size).
 // Blocks [0, nq) walk q's (token tile, run of heads) units, the next nk k's, the rest v's.
 // A head row takes p.rep steps, one for each of the attention's heads that share it; the
 // norm's backward follows the last.  Each block of q and k sums its share of the norm
@@ -441,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
             }
             copies_commit();
         };
+        copies_wait<0>();  // (a slot's zeros past the last unit's end come before what follows)
 #pragma unroll
         for (int n = 0; n < R::kDepth; ++n) prefetch();
         if (turn) {
@@ -497,7 +507,9 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
                     ss = ffma2(x2[j], x2[j], ss);
                     ux = ffma2(u[j], x2[j], ux);
                 }
-                const float r = rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + s.eps);
+                // (a row that is not there holds zeros: with eps = 0 its r would be infinite)
+                const float mean = row_sum<L>(ss.x + ss.y) * (1.f / D) + s.eps;
+                const float r = row * kSlots < mine ? rsqrtf(mean) : 0.f;
                 const float m = row_sum<L>(ux.x + ux.y) * r * (1.f / D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {

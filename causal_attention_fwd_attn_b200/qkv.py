@@ -42,5 +42,5 @@ def qkv_bwd(dq, dk, dv, q, k, q_weight=None, k_weight=None, *, eps=1e-6, inv_fre
 
 
 def qkv_workspace_bytes(d) -> int:
-    """Bytes of qkv_bwd's workspace for head dimension d on the current device."""
+    """Bytes of qkv_bwd's workspace for head dimension d."""
     return _lib.forge_qkv_bwd_workspace_size(d)

@@ -220,8 +220,8 @@ int forge_attn_bf16_to_fp16(const void* src, void* dst, long long n, unsigned in
  * The stage between the QKV projection and the attention, in one pass each way: an RMS
  * norm of every query and key head, rotary positions with one or several axes, and the
  * change of layout from the projection's token-major rows to the attention's
- * [B][H][T][d].  (The paper's model adds learned positions to its embeddings and has no
- * counterpart; models with rotary positions need this stage around its attention.)
+ * [B][H][T][d].  (The paper has no counterpart: models with rotary positions need this stage
+ * before its attention.)
  *
  *   r = 1 / sqrt(mean_i x_i^2 + eps),  n = r x o weight          (weight NULL: n = x)
  *   pair j of the first `rot` elements, (a, b):  phi = positions[axis_j][b][t] * inv_freq[j],
@@ -273,8 +273,8 @@ int forge_qkv_fwd(const forge_qkv_config* config, const forge_qkv_tensor* q,
                   const forge_qkv_tensor* k, const forge_qkv_tensor* v, void* q_out, void* k_out,
                   void* v_out, int flags, void* stream);
 
-/* Bytes of device workspace forge_qkv_bwd needs on the current device for head dimension d
- * (0 if it is not 64 or 128); only read where a norm weight is given. */
+/* Bytes of device workspace forge_qkv_bwd needs for head dimension d (0 if it is not 64 or
+ * 128); only looked at where a norm weight is given. */
 size_t forge_qkv_bwd_workspace_size(int d);
 
 /*

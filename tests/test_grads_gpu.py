@@ -189,6 +189,13 @@ def test_refusals():
         fa.grad_norm([g[1:]])
     with pytest.raises(fa.ForgeAttnError, match="workspace"):
         fa.grad_norm([g], workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    # any iterable of tensors is held until the launch
+    grads, out = make([5000, 300], KINDS, 13), [torch.empty(5000, device=DEV), None]
+    out[1] = torch.empty(300, dtype=KINDS[1], device=DEV)
+    fa.grad_clip((t for t in grads), 0.1, out=(t for t in out))
+    want = [t.clone() for t in grads]
+    fa.grad_clip(want, 0.1)
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
     # reading one tensor twice is a sum like any other
     one = torch.full((4,), 3.0, device=DEV)
     assert fa.grad_norm([one, one]).item() == pytest.approx(72 ** 0.5, rel=4e-6)

@@ -213,6 +213,19 @@ def test_values_that_are_not_finite_stay_in_their_place():
         assert torch.isfinite(t).all()
 
 
+def test_a_norm_without_eps_beside_rows_that_are_not_there():
+    """Tokens past the last and heads past the last must not enter the weights' gradients."""
+    B, T, H, d = 1, 19, 3, 64
+    x = torch.randn((B, T, H, d), device=DEV).to(torch.bfloat16)
+    g = torch.randn((B, H, T, d), device=DEV)
+    w = torch.ones(d, device=DEV)
+    gq, gk, gv, gwq, gwk = fa.qkv_bwd(g, g, g, x, x, w, w, eps=0.0)
+    ref, ref_w = oq.head_bwd(f64(g), f64(x), f64(w), None, False, 0.0)
+    total = np.abs(f64(g)).sum((0, 1, 2)) * 4
+    assert (np.abs(f64(gwq) - ref_w) <= 1e-5 * total).all() and torch.equal(gwq, gwk)
+    assert torch.isfinite(gq).all() and torch.equal(gq, gk)
+
+
 def test_pair_axes_out_of_range_count_as_the_nearest():
     x = torch.randn((1, 5, 1, 64), device=DEV).to(torch.bfloat16)
     freq = torch.rand(32, dtype=torch.float64, device=DEV)
