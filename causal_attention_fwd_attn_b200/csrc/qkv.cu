@@ -356,7 +356,7 @@ struct Bwd {
 
 // Backward.  B2 T4096 H16 d128 (268 MB) takes 49 us, 5.4 TB/s or 0.83 of the copy rate, with fp32
 // gradients (369 MB) 63 us, 0.89 of it; B3 T1023 H12 Hkv4 d64 with fp32 gradients (42 MB) 15 us, most of
-// it latencies.  The norm's arithmetic keeps a third of the issue slots busy, so angles and
+// it latencies.  Two thirds of the issue slots are busy (a third of them with the norm), so angles and
 // weights are read from shared memory and three blocks fit on an SM (in registers, with two
 // blocks: 62 us at the first size).
 // Blocks [0, nq) walk q's (token tile, run of heads) units, the next nk k's, the rest v's.
