@@ -46,6 +46,7 @@ namespace forge {
 namespace {
 
 constexpr int kMaxExperts = FORGE_LINEAR_MAX_EXPERTS;
+constexpr int kMaxFeatures = FORGE_LINEAR_GROUPED_MAX_FEATURES;
 // Warps: 0 copies, 1 issues the products (in the pair's first block), 2 clears tails (dW), from
 // 4 on the epilogue, in groups of four (warp w reads tensor memory lanes 32 (w % 4)..).
 constexpr int kGroups = 2;
@@ -696,6 +697,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int check_dims(int rows, int experts, int in_f, int out_f) {
     if (rows < 0 || experts < 1 || in_f < 1 || out_f < 1) return FORGE_ATTN_ERR_INVALID_ARG;
     if (experts > kMaxExperts || in_f % 8 || out_f % 8) return FORGE_ATTN_ERR_UNSUPPORTED;
+    // (the longest reduction of one accumulator has to end well inside the limit of a wait)
+    if (in_f > kMaxFeatures || out_f > kMaxFeatures) return FORGE_ATTN_ERR_UNSUPPORTED;
     if ((long long)rows * in_f >= (1ll << 31) || (long long)rows * out_f >= (1ll << 31) ||
         (long long)out_f * in_f >= (1ll << 31))
         return FORGE_ATTN_ERR_UNSUPPORTED;

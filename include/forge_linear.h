@@ -66,13 +66,14 @@ int forge_linear_split_k(int tokens, int in_features, int out_features);
  * them, none included.  They are read on the device only; each is clamped to [0, rows], so
  * that no contents can lead outside the tensors.  rows: the token matrices' rows; those that
  * belong to no expert are not read as data and not written.  Rows need not be a multiple of
- * anything; in_features and out_features are multiples of 8; experts <= 1024.
+ * anything; in_features and out_features are multiples of 8, at most 2^20; experts <= 1024.
  *   w, dw [experts][out_features][in_features]; each matrix, and each token matrix, below
  *   2^31 elements.
  * rows = 0 is allowed (x, dy, y, dx may then be NULL).  Other conventions as above.  One launch
  * each (a memset for dw when rows = 0); deterministic.
  */
 #define FORGE_LINEAR_MAX_EXPERTS 1024
+#define FORGE_LINEAR_GROUPED_MAX_FEATURES (1 << 20)
 
 /* y[r] = x[r] w_e^T for the rows r of each expert e.  flags: FORGE_ATTN_OUT_F32, FORGE_ATTN_FP16. */
 int forge_linear_grouped_fwd(const void* x, const void* w, void* y, const int* offsets, int rows,

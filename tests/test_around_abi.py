@@ -112,6 +112,8 @@ def test_grouped_rejects_bad_arguments():
         assert fn(P, P, P, P, 8, 4, 60, 64, 0, None) == _lib.ERR_UNSUPPORTED
         assert fn(P, P, P, P, 8, 4, 64, 12, 0, None) == _lib.ERR_UNSUPPORTED
         assert fn(P, P, P, P, 1 << 25, 4, 64, 64, 0, None) == _lib.ERR_UNSUPPORTED
+        assert fn(P, P, P, P, 8, 4, 1 << 21, 64, 0, None) == _lib.ERR_UNSUPPORTED
+        assert fn(P, P, P, P, 8, 4, 64, 1 << 21, 0, None) == _lib.ERR_UNSUPPORTED
         assert fn(P, P, P, P, 8, 4, 64, 64, _lib.PRECISE, None) == _lib.ERR_INVALID_ARG
         assert fn(P, P + 8, P, P, 8, 4, 64, 64, 0, None) == _lib.ERR_MISALIGNED
         assert fn(P, P, P, P + 2, 8, 4, 64, 64, 0, None) == _lib.ERR_MISALIGNED
