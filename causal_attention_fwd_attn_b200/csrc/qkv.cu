@@ -238,6 +238,7 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 constexpr int kFwdDepth = 4;
+constexpr int kFwdBlocksPerSm = 3;
 
 // Forward.  HBM is the bound of large calls: B1 T8000 H32 d128 (393 MB) takes 64.7 us, 6.08 TB/s or
 // 0.93 of the copy rate; loads, arithmetic and stores in one thread without the ring, and
@@ -248,7 +249,7 @@ constexpr int kFwdDepth = 4;
 // Runs of heads that the blocks of a token tile take: nq runs of q's heads, nk of k's and the
 // rest of v's, `per` heads to a run.
 template <int D, bool F16, bool ADJ>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
     qkv_fwd_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int nq, int nk,
                    int runs, int per) {
     using C = Cfg<D>;
@@ -664,30 +665,29 @@ Part make_part(const forge_qkv_tensor* x, const float* w, int heads, int rep) {
     return p;
 }
 
-// Blocks of the backward and the heads of a unit's run.  A unit costs kStart (its latencies
-// and its angles) and its rows, in the time of one row of eight to a thread or fewer: the choice
-// is the one with the least work for a resident block plus one unit, the wait for the last.  A block
-// has one unit while that keeps the partial sums of the weights' gradients few.
-struct Blocks {
-    int n[3], per;
+// Heads of a run, and the units (token tile, run) of each part.  A unit costs kStart (its
+// latencies and its angles) and its rows, in the time of one row of eight to a thread or
+// fewer: the choice is the one with the least work for a resident block plus one unit, the
+// wait for the last.
+struct Split {
+    long long units[3];
+    int per;
 };
-constexpr double kStart = 3.0;
-constexpr int kMaxPartials = 1024;  // of q, and of k
-Blocks share_out(const double* row_cost, const int* heads, long long tiles, int resident) {
-    Blocks best{};
+constexpr double kStart = 4.5;
+Split split_heads(const double* row_cost, const int* heads, long long tiles, int resident) {
+    Split best{};
     double best_time = 0.0;
     for (int rows = 8; rows >= 1; rows /= 2) {
-        Blocks b{};
+        Split b{};
         b.per = rows * kSlots;
         double sum = 0.0, most = 0.0;
         for (int j = 0; j < 3; ++j) {
             if (row_cost[j] <= 0.0) continue;
-            const long long units = tiles * ((heads[j] + b.per - 1) / b.per);
+            b.units[j] = tiles * ((heads[j] + b.per - 1) / b.per);
             const int used = heads[j] < b.per ? (heads[j] + kSlots - 1) / kSlots : rows;
             const double cost = kStart + used * row_cost[j];
-            sum += units * cost;
+            sum += b.units[j] * cost;
             most = cost > most ? cost : most;
-            b.n[j] = (int)(units < kMaxPartials ? units : kMaxPartials);
         }
         const double time = sum / resident + most;
         if (rows == 8 || time < best_time) {
@@ -698,13 +698,12 @@ Blocks share_out(const double* row_cost, const int* heads, long long tiles, int 
     return best;
 }
 
-// Heads of a block's run: eight rows to a thread, fewer (down to one) where that would leave
-// less than `want` blocks.
-int heads_to_a_block(int heads, long long tiles, long long want) {
-    int rows = 8;
-    while (rows > 1 && tiles * ((heads + rows * kSlots - 1) / (rows * kSlots)) < want) rows /= 2;
-    return rows * kSlots;
-}
+// Blocks of the backward: one to a unit while that keeps the partial sums of the weights'
+// gradients few.
+constexpr int kMaxPartials = 1024;  // of q, and of k
+struct Blocks {
+    int n[3], per;
+};
 
 template <int D, bool F16, bool G32, bool ADJ>
 cudaError_t launch_bwd_t(const Parts& parts, const Rope& rope, const Shape& s, const Blocks& n,
@@ -751,14 +750,16 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
     const long long tokens = (long long)c->B * c->T, tok = c->d == 64 ? Cfg<64>::kTok : Cfg<128>::kTok,
                     tiles = (tokens + tok - 1) / tok;
     Parts parts;
-    int all = 0, n[3];
-    for (int j = 0; j < 3; ++j) all += in[j] ? heads[j] : 0;
-    const int per = heads_to_a_block(all, tiles, 4LL * sm_count());
+    double row_cost[3];
     for (int j = 0; j < 3; ++j) {
         parts.part[j] = make_part(in[j], weight[j], heads[j], c->H / heads[j]);
         parts.part[j].y = out[j];
-        n[j] = in[j] ? (heads[j] + per - 1) / per : 0;
+        row_cost[j] = in[j] ? 0.5 + 0.5 * parts.part[j].rep : 0.0;
     }
+    const Split split = split_heads(row_cost, heads, tiles, kFwdBlocksPerSm * sm_count());
+    const int per = split.per;
+    int n[3];
+    for (int j = 0; j < 3; ++j) n[j] = in[j] ? (heads[j] + per - 1) / per : 0;
     const Shape s{c->T, c->H, (unsigned)tokens, c->eps};
     const Rope rope = make_rope(*c);
     const int runs = n[0] + n[1] + n[2];
@@ -838,8 +839,11 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
         }
         row_cost[j] = out[j] ? 0.5 * p[j].rep + (norm ? 0.5 : 0.0) : 0.0;
     }
-    const Blocks n =
-        share_out(row_cost, heads, tiles, resident);
+    const Split split = split_heads(row_cost, heads, tiles, resident);
+    Blocks n;
+    n.per = split.per;
+    for (int j = 0; j < 3; ++j)
+        n.n[j] = (int)(split.units[j] < kMaxPartials ? split.units[j] : kMaxPartials);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     float* ws = static_cast<float*>(workspace);
 #define FORGE_QKV_BWD(D_)                                                                \
