@@ -112,6 +112,8 @@ __device__ __forceinline__ void pairs_of(int i, int pairs, int& a, int& b) {
 // Tables in shared memory: what thread i of a row reads lies in four 16-byte columns, each
 // with the threads of a row side by side.
 // Angles, [kTok][4][kLanes] of (cos, cos, sin, sin) of two pairs.  A warp takes every eighth token.
+// Past the last token the turn is none: rows that are not there are rotated too, and their
+// zeros have to stay zeros in the sums over the rows.
 template <int D, bool ADJ>
 __device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsigned tok0,
                                             float* cs) {
@@ -144,8 +146,8 @@ __device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsig
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            if (!on[n][m]) continue;
-            double v = turns[n][m] * (f[m] * 0.15915494309189533577);
+            if ((int)lane_id() + 32 * m >= r.pairs) continue;
+            double v = on[n][m] ? turns[n][m] * (f[m] * 0.15915494309189533577) : 0.;
             v -= rint(v);
             float sn, c;
             sincospif(2.f * (float)v, &sn, &c);

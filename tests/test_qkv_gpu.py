@@ -226,6 +226,31 @@ def test_a_norm_without_eps_beside_rows_that_are_not_there():
     assert torch.isfinite(gq).all() and torch.equal(gq, gk)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("grad32", [False, True])
+def test_what_shared_memory_held_before_does_not_matter(d, adjacent, grad32):
+    """Calls whose rows, weights and angles are NaN leave NaN in every SM's shared memory; the
+    tokens that a later call's last tile lacks must not bring them into its sums."""
+    bad = torch.full((1, 6000, 4, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wbad = torch.full((d,), float("nan"), device=DEV)
+    fbad = torch.full((d // 2,), float("nan"), dtype=torch.float64, device=DEV)
+    gbad = torch.full((1, 4, 6000, d), float("nan"), device=DEV)
+    x = torch.randn((1, 3, 3, d), device=DEV).to(torch.bfloat16)
+    g = torch.randn((1, 3, 3, d), device=DEV).to(torch.float32 if grad32 else torch.bfloat16)
+    w = torch.ones(d, device=DEV)
+    f = torch.rand(d // 2, dtype=torch.float64, device=DEV)
+    ref, ref_w = oq.head_bwd(f64(g), f64(x), f64(w), oq.angles(f64(f), None, None, 1, 3), adjacent, EPS)
+    for _ in range(3):
+        fa.qkv_fwd(bad, bad, bad, wbad, wbad, inv_freq=fbad, adjacent=adjacent)
+        fa.qkv_bwd(gbad, gbad, gbad, bad, bad, wbad, wbad, inv_freq=fbad, adjacent=adjacent)
+        gq, gk, gv, gwq, gwk = fa.qkv_bwd(g, g, g, x, x, w, w, inv_freq=f, adjacent=adjacent)
+        q, _, _ = fa.qkv_fwd(x, x, x, w, w, inv_freq=f, adjacent=adjacent)
+        assert all(torch.isfinite(t).all() for t in (gq, gk, gv, gwq, gwk, q))
+        total = 4 * np.abs(f64(g)).sum((0, 1, 2))
+        assert (np.abs(f64(gwq) - ref_w) <= 1e-5 * total.max()).all()
+
+
 def test_pair_axes_out_of_range_count_as_the_nearest():
     x = torch.randn((1, 5, 1, 64), device=DEV).to(torch.bfloat16)
     freq = torch.rand(32, dtype=torch.float64, device=DEV)
