@@ -487,6 +487,33 @@ const Tensor& flat(PyObject* o, int index, const char* what) {
            std::to_string(index));
 }
 
+// In place or not: nothing may be scaled twice, nor written while it is still to be read.
+void check_writes(const std::vector<forge_grad_tensor>& table) {
+    struct Span {
+        uintptr_t from, to;
+        bool operator<(const Span& o) const { return from < o.from; }
+    };
+    auto span = [](const forge_grad_tensor& t, const void* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return Span{at, at + (uintptr_t)t.n * (t.dtype == FORGE_GRAD_F32 ? 4 : 2)};
+    };
+    std::vector<Span> written;
+    written.reserve(table.size());
+    for (const forge_grad_tensor& t : table)
+        if (t.n) written.push_back(span(t, t.out));
+    if (!std::is_sorted(written.begin(), written.end())) std::sort(written.begin(), written.end());
+    for (size_t k = 1; k < written.size(); ++k)
+        if (written[k].from < written[k - 1].to) refuse("the same tensor is written twice");
+    for (const forge_grad_tensor& t : table) {
+        if (!t.n || t.grad == t.out) continue;
+        const Span s = span(t, t.grad);
+        const auto next = std::lower_bound(written.begin(), written.end(), s);
+        if ((next != written.end() && next->from < s.to) ||
+            (next != written.begin() && std::prev(next)->to > s.from))
+            refuse("an output overlaps a gradient that is read for another");
+    }
+}
+
 // (grads, clip, max_norm, out, norm, workspace): clip False computes the norm alone.
 PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return guarded([&]() -> PyObject* {
@@ -517,15 +544,7 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                 table[k].out = t.data_ptr();
             }
         }
-        if (clip) {  // in place or not: nothing may be scaled twice
-            std::vector<const void*> written;
-            written.reserve((size_t)n);
-            for (const forge_grad_tensor& t : table)
-                if (t.n) written.push_back(t.out);
-            std::sort(written.begin(), written.end());
-            if (std::adjacent_find(written.begin(), written.end()) != written.end())
-                refuse("the same tensor is written twice");
-        }
+        if (clip) check_writes(table);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
         Tensor norm, ws;
         if (given(a[4])) {

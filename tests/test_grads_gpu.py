@@ -189,6 +189,20 @@ def test_refusals():
         fa.grad_norm([g[1:]])
     with pytest.raises(fa.ForgeAttnError, match="workspace"):
         fa.grad_norm([g], workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    # slices that overlap, in place and as outputs; neighbours do not
+    whole, other = torch.ones(64, device=DEV), torch.ones(64, device=DEV)
+    with pytest.raises(ValueError, match="twice"):
+        fa.grad_clip([whole[32:64], whole[:36]], 1.0)
+    with pytest.raises(ValueError, match="twice"):
+        fa.grad_clip([g[:8], whole[:8]], 1.0, out=[other[:8], other[4:12]])
+    with pytest.raises(ValueError, match="read for another"):
+        fa.grad_clip([whole[:16], whole[16:32]], 1.0, out=[other[:16], whole[8:24]])
+    with pytest.raises(ValueError, match="read for another"):
+        fa.grad_clip([whole[:16], whole[16:32]], 1.0, out=[whole[28:44], other[:16]])
+    assert (whole == 1).all() and (other == 1).all()
+    assert fa.grad_clip([whole[32:], whole[:32]], 4.0).item() == 8.0
+    assert (whole == 0.5).all()
+    assert fa.grad_clip([whole[:16], whole[16:32]], 4.0, out=[whole[:16], other[:16]]).item() < 4.0
     # any iterable of tensors is held until the launch
     grads, out = make([5000, 300], KINDS, 13), [torch.empty(5000, device=DEV), None]
     out[1] = torch.empty(300, dtype=KINDS[1], device=DEV)
