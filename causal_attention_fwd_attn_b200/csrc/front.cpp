@@ -413,6 +413,8 @@ PyObject* grouped_rows(PyObject* const* a, Py_ssize_t n) {
     if (given(a[3])) {
         y = tensor(a[3], "out");
         check(y, "out", {p.a.scalar_type(), kF32}, p.index, &shape);
+        if (given(a[4]) && truth(a[4]) != (y.scalar_type() == kF32))
+            refuse("out and out_dtype differ");
     } else {
         y = empty(shape, given(a[4]) && truth(a[4]) ? kF32 : p.a.scalar_type(), p.index);
     }

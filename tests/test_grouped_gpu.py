@@ -274,6 +274,8 @@ def test_front_end_refusals_on_cuda_tensors():
             (lambda: fa.linear_grouped_fwd(x[:, ::2], w, off), "contiguous"),
             (lambda: fa.linear_grouped_fwd(x, w, off, out=dy[:4]), "shape"),
             (lambda: fa.linear_grouped_fwd(x, w, off, out_dtype=torch.float16), "out_dtype"),
+            (lambda: fa.linear_grouped_fwd(x, w, off, torch.empty_like(dy), torch.float32), "out_dtype"),
+            (lambda: fa.linear_grouped_bwd_dx(dy, w, off, x.float(), x.dtype), "out_dtype"),
             (lambda: fa.linear_grouped_bwd_dx(x, w, off), "features"),
             (lambda: fa.linear_grouped_bwd_dw(dy[:7], x, off), "rows"),
             (lambda: fa.linear_grouped_bwd_dw(dy, x, off, accumulate=True), "out"),
