@@ -239,6 +239,30 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A thread's share of one head of q or k: norm, weights, rotation.
+template <int D, bool F16, bool ADJ>
+__device__ __forceinline__ void forward_row(uint4& oa, uint4& ob, bool norm, const float4* my_w,
+                                            const float4* my_cs, int na, int nb, float eps) {
+    float2 f[8];
+    unpack8<F16>(oa, f);
+    unpack8<F16>(ob, f + 4);
+    if (norm) {
+        float2 ss = fmul2(f[0], f[0]);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) ss = ffma2(f[j], f[j], ss);
+        const float2 r = both(rsqrtf(row_sum<Cfg<D>::kLanes>(ss.x + ss.y) * (1.f / D) + eps));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 w = my_w[c];
+            f[2 * c] = fmul2(fmul2(f[2 * c], r), make_float2(w.x, w.y));
+            f[2 * c + 1] = fmul2(fmul2(f[2 * c + 1], r), make_float2(w.z, w.w));
+        }
+    }
+    rotate<1, ADJ, false>(f, my_cs, na, nb);
+    oa = pack8<F16>(f);
+    ob = pack8<F16>(f + 4);
+}
+
 constexpr int kFwdDepth = 4;
 constexpr int kFwdBlocksPerSm = 3;
 
@@ -316,24 +340,7 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
         uint4* at = &ring[n % kFwdDepth][0][threadIdx.x];
         uint4 oa = at[0], ob = at[kThreads];
         if (kind < 2) {
-            float2 f[8];
-            unpack8<F16>(oa, f);
-            unpack8<F16>(ob, f + 4);
-            if (norm) {
-                float2 ss = fmul2(f[0], f[0]);
-#pragma unroll
-                for (int j = 1; j < 8; ++j) ss = ffma2(f[j], f[j], ss);
-                const float2 r = both(rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + s.eps));
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 w = my_w[c];
-                    f[2 * c] = fmul2(fmul2(f[2 * c], r), make_float2(w.x, w.y));
-                    f[2 * c + 1] = fmul2(fmul2(f[2 * c + 1], r), make_float2(w.z, w.w));
-                }
-            }
-            rotate<1, ADJ, false>(f, my_cs, na, nb);
-            oa = pack8<F16>(f);
-            ob = pack8<F16>(f + 4);
+            forward_row<D, F16, ADJ>(oa, ob, norm, my_w, my_cs, na, nb, s.eps);
         }
         if (n * kSlots < mine) {
             for (int c = 0; c < p.rep; ++c, y += head) {
@@ -343,6 +350,110 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
             y += (kSlots - 1) * p.rep * head;
         }
         prefetch(n % kFwdDepth);  // into the slots just read
+    }
+    copies_wait<0>();
+}
+
+// The same where q, k and v are few heads (a tensor-parallel rank's): a block takes a token tile's
+// heads of all three, so that they share its start and its angles.  A row is kSlots heads of
+// one part; rows are q's (the first `qe`), k's (up to `ke`), then v's (up to `ve`).
+// Chosen for up to kFewRows rows where there are two such blocks and more for every resident one:
+// B16 T2048 H4 Hkv1 d128 (2048 tiles) 35.1 us against 43.8 with a block to each part, B64 T2048 H3 d64
+// 69.5 against 89.6, H16 Hkv2 d128 (ten rows) 346 against 368 there and 91.7 against 92.1 at B16; with
+// 512 tiles (B8 T1024 H8 Hkv1 d128) 18.0 against 17.3, with 188 (B1 T3000) 9.4 against 7.6.  Walking
+// the parts costs registers and instructions: runs of a larger list of rows, across the
+// parts, took 36.6 where the kernel above takes 34.3 (B2 T4096 H16 d128).
+constexpr int kFewRows = 10;
+template <int D, bool F16, bool ADJ>
+__global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
+    qkv_fwd_few_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int qe,
+                       int ke, int ve) {
+    using C = Cfg<D>;
+    constexpr int L = C::kLanes, kTok = C::kTok;
+    __shared__ float4 cs[kTok * 4 * L];
+    __shared__ float4 wt[2][4 * L];
+    __shared__ uint4 ring[kFwdDepth][2][kThreads];
+    allow_dependents_launch();
+    grid_dependency_wait();
+    const unsigned tok0 = blockIdx.x * kTok;
+    const int i = threadIdx.x % L, g = threadIdx.x / L;
+    const int t = g % kTok, slot = g / kTok;
+    const bool here = tok0 + t < s.tokens;
+    const unsigned tok = min(tok0 + t, s.tokens - 1);
+    const unsigned b = tok / (unsigned)s.T, tt = tok - b * (unsigned)s.T;
+    int ea, eb;
+    chunks_of<D, ADJ>(i, rope.pairs, ea, eb);
+    auto kind_of = [&](int row) { return row < qe ? 0 : (row < ke ? 1 : 2); };
+    auto end_of = [&](int kind) { return kind == 0 ? qe : (kind == 1 ? ke : ve); };
+
+    // What is fetched next: the row, its part's end, the thread's head of how many.
+    int f_row = 0, f_end, f_head, f_heads;
+    const uint16_t* x;
+    long long x_step;
+    auto fetch_part = [&]() {  // from its first row on
+        const int kind = kind_of(f_row);
+        const Part& p = parts.part[kind];
+        f_end = end_of(kind);
+        f_head = slot;
+        f_heads = here ? p.heads : 0;
+        x_step = kSlots * p.sh;
+        x = static_cast<const uint16_t*>(p.x) + b * p.sb + tt * p.st +
+            (slot < p.heads ? slot * p.sh : 0);
+    };
+    auto prefetch = [&](int at) {
+        const bool on = f_row < ve && f_head < f_heads;
+        copy16(&ring[at][0][threadIdx.x], x + ea, on);
+        copy16(&ring[at][1][threadIdx.x], x + eb, on);
+        copies_commit();
+        if (++f_row == f_end && f_row < ve) {
+            fetch_part();
+        } else {
+            f_head += kSlots;
+            if (f_head < f_heads) x += x_step;  // (past the last row the address stays valid)
+        }
+    };
+    fetch_part();
+#pragma unroll
+    for (int n = 0; n < kFwdDepth; ++n) prefetch(n);
+    if (rope.pairs > 0 && ke > 0) fill_angles<D, ADJ>(rope, s, tok0, reinterpret_cast<float*>(cs));
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+        if (parts.part[kind].w)
+            fill_weights<D, ADJ>(parts.part[kind].w, rope.pairs, reinterpret_cast<float*>(wt[kind]));
+    __syncthreads();
+    int na, nb;  // the thread's rotated pairs
+    pairs_of<D, ADJ>(i, rope.pairs, na, nb);
+    float4 my_cs[4], my_w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) my_cs[c] = cs[(t * 4 + c) * L + i];
+    const long long head = (long long)s.T * D;
+
+    int row = 0, at_now = 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        const Part& p = parts.part[kind];
+        const int end = end_of(kind), heads = here ? p.heads : 0;
+        const bool norm = p.w != nullptr;
+        if (norm) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) my_w[c] = wt[kind][c * L + i];
+        }
+        uint16_t* y = static_cast<uint16_t*>(p.y) +
+                      (((long long)b * s.H + (long long)slot * p.rep) * s.T + tt) * D;
+        for (int h = slot; row < end; ++row, h += kSlots) {
+            copies_wait<kFwdDepth - 1>();
+            uint4* at = &ring[at_now][0][threadIdx.x];
+            uint4 oa = at[0], ob = at[kThreads];
+            if (kind < 2) forward_row<D, F16, ADJ>(oa, ob, norm, my_w, my_cs, na, nb, s.eps);
+            if (h < heads) {
+                for (int c = 0; c < p.rep; ++c, y += head) {
+                    *reinterpret_cast<uint4*>(y + ea) = oa;
+                    *reinterpret_cast<uint4*>(y + eb) = ob;
+                }
+                y += (kSlots - 1) * p.rep * head;
+            }
+            prefetch(at_now);  // into the slots just read
+            at_now = (at_now + 1) % kFwdDepth;
+        }
     }
     copies_wait<0>();
 }
@@ -770,6 +881,18 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0;
     const bool adj = (flags & FORGE_QKV_ADJACENT) != 0;
+    int ends[3], rows = 0;
+    for (int j = 0; j < 3; ++j)
+        ends[j] = rows += in[j] ? (heads[j] + kSlots - 1) / kSlots : 0;
+    if (rows <= kFewRows && tiles >= 2 * kFwdBlocksPerSm * sm_count()) {
+#define FORGE_QKV_FWD(D_)                                                                       \
+    (f16 ? (adj ? qkv_fwd_few_kernel<D_, true, true> : qkv_fwd_few_kernel<D_, true, false>)     \
+         : (adj ? qkv_fwd_few_kernel<D_, false, true> : qkv_fwd_few_kernel<D_, false, false>))
+        auto* kernel = c->d == 64 ? FORGE_QKV_FWD(64) : FORGE_QKV_FWD(128);
+#undef FORGE_QKV_FWD
+        return status_of(launch_dependent(kernel, dim3((unsigned)tiles), dim3(kThreads), 0, cs, parts,
+                                          rope, s, ends[0], ends[1], ends[2]));
+    }
 #define FORGE_QKV_FWD(D_)                                                                 \
     (f16 ? (adj ? qkv_fwd_kernel<D_, true, true> : qkv_fwd_kernel<D_, true, false>)       \
          : (adj ? qkv_fwd_kernel<D_, false, true> : qkv_fwd_kernel<D_, false, false>))

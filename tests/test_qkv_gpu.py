@@ -251,6 +251,36 @@ def test_what_shared_memory_held_before_does_not_matter(d, adjacent, grad32):
         assert (np.abs(f64(gwq) - ref_w) <= 1e-5 * total.max()).all()
 
 
+@pytest.mark.parametrize("H,Hkv,d,rot,adjacent,dtype", [
+    (1, 1, 64, 64, False, torch.bfloat16), (2, 1, 64, 32, False, torch.float16),
+    (3, 3, 128, 128, False, torch.bfloat16), (4, 1, 128, 54, True, torch.bfloat16),
+    (5, 5, 64, 64, True, torch.float16), (16, 2, 128, 128, False, torch.float16),
+    (17, 1, 64, 64, False, torch.bfloat16), (8, 4, 64, 0, False, torch.bfloat16)])
+def test_few_heads_of_many_tokens(H, Hkv, d, rot, adjacent, dtype):
+    """Token tiles whose heads one block takes whole, and a list just too long for that: the same bits
+    as a call on each sequence, and within the bounds at a sequence's first and last tokens."""
+    B, T = 8, 4099
+    g, q, k, v, wq, wk, kw, phi = make((B, T, H, Hkv, d, rot, 2 if rot else 0, dtype, adjacent, "packed",
+                                        True, True), 23)
+    n, few = 70, {name: kw[name] for name in kw if name != "positions"}
+    for weights in ((wq, wk), (None, wk), (wq, None)):
+        got = fa.qkv_fwd(q, k, v, *weights, eps=EPS, **kw)
+        for b in range(B):
+            if rot:
+                few["positions"] = kw["positions"][:, b:b + 1].contiguous()
+            own = fa.qkv_fwd(q[b:b + 1], k[b:b + 1], v[b:b + 1], *weights, eps=EPS, **few)
+            assert all(torch.equal(x[b:b + 1], y) for x, y in zip(got, own)), b
+        for part in (slice(0, n), slice(T - n, T)):
+            turn = None if phi is None else phi[B - 1:, part]
+            for x, w, o, a in ((q, weights[0], got[0], turn), (k, weights[1], got[1], turn),
+                               (v, None, got[2], None)):
+                x, o = x[B - 1:, part], o[B - 1:, :, part]
+                rep = H // x.shape[2]
+                ref = oq.head_fwd(f64(x), f64(w), a, adjacent, EPS, rep)
+                slack = 4e-6 * np.repeat(np.swapaxes(bound_head(x, w, dtype), 1, 2), rep, axis=1)
+                within(o, ref, slack, dtype, f"{H} {Hkv} {d}")
+
+
 def test_pair_axes_out_of_range_count_as_the_nearest():
     x = torch.randn((1, 5, 1, 64), device=DEV).to(torch.bfloat16)
     freq = torch.rand(32, dtype=torch.float64, device=DEV)
@@ -331,6 +361,23 @@ def test_parts_may_be_left_out():
     assert _lib.forge_qkv_bwd(cfg, None, None, y.data_ptr(), None, None, None, None, tb, None, None, 0,
                               None, 0, 0, s) == _lib.OK
     assert torch.equal(back, x)
+
+
+def test_parts_of_few_heads_may_be_left_out():
+    B, T, H, Hkv, d = 8, 4099, 3, 1, 64
+    _, q, k, v, wq, wk, kw, _ = make((B, T, H, Hkv, d, d, 1, torch.bfloat16, False, "packed", True, True), 29)
+    want = fa.qkv_fwd(q, k, v, wq, wk, eps=EPS, **kw)
+    cfg = _lib.QkvConfig(B, T, H, Hkv, d, d, 1, EPS, kw["inv_freq"].data_ptr(), kw["positions"].data_ptr(),
+                         kw["pair_axis"].data_ptr(), wq.data_ptr(), wk.data_ptr())
+    ins = [_lib.QkvTensor(x.data_ptr(), *x.stride()[:3]) for x in (q, k, v)]
+    for keep in range(1, 8):
+        outs = [torch.full_like(o, -7.0) for o in want]
+        on = [keep >> j & 1 for j in range(3)]
+        assert _lib.forge_qkv_fwd(cfg, *(t if f else None for t, f in zip(ins, on)),
+                                  *(o.data_ptr() if f else None for o, f in zip(outs, on)), 0,
+                                  torch.cuda.current_stream().cuda_stream) == _lib.OK
+        for o, w, f in zip(outs, want, on):
+            assert torch.equal(o, w) if f else (o == -7).all(), keep
 
 
 def test_one_graph_beside_eager_calls_of_the_same_tensors():
