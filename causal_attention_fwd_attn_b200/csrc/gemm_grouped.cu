@@ -66,7 +66,10 @@ struct Barriers {
     uint64_t mma_final;
     uint32_t tmem_base;
     int abort;
-    int cost[8];  // of the choices of choose_width
+    union {
+        int cost[8];  // of the choices of choose_width (rows kernel)
+        int begun;    // k-blocks whose copies this block's producer has begun (dW)
+    };
 };
 static_assert(sizeof(Barriers) <= 320, "barrier block");
 constexpr int kBarBytes = 320;
@@ -149,6 +152,7 @@ __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int sta
         }
         mbar_init(&bars->mma_final, 1);
         bars->abort = 0;
+        bars->begun = 0;
         fence_mbar_init();
     }
     if (warp_id() == 1) {
@@ -165,8 +169,10 @@ __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int sta
 }
 
 // End of both kernels: neither block leaves (or gives up tensor memory) while the other may
-// still read or signal it.
+// still read or signal it.  The wait for the last signal begins when the block's own work has
+// ended (the second block's warp 1 has none, and a launch may take longer than a wait's limit).
 __device__ __forceinline__ void finish(Barriers* bars) {
+    __syncthreads();
     if (warp_id() == 1) mbar_wait_drain(&bars->mma_final, 0);  // all products and signals
     tc_fence_before();
     __syncthreads();
@@ -497,6 +503,30 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, uint32_t l
                 make_uint4(0, 0, 0, 0);
 }
 
+// Waits for a tail's copies.  They come after all others of the expert's reduction, and of units
+// without a tail before it: 4 million k-blocks and more, longer than one wait may take.
+// The limit therefore counts from the last k-block that the producer began.
+__device__ __forceinline__ bool wait_landed(uint64_t* bar, uint32_t parity, const volatile int* begun,
+                                            volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    int seen = *begun;
+    uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) != 0) continue;
+        if (*abort) return false;
+        const int now = *begun;
+        if (now != seen) {
+            seen = now;
+            t0 = globaltimer_ns();
+        } else if (globaltimer_ns() - t0 > FORGE_WAIT_LIMIT_NS) {
+            record_timeout(kSiteLanded);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
 template <bool ADD, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_dw_kernel(const __grid_constant__ CUtensorMap tmap_dy,
@@ -510,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* const staging0 = smem + stages * kDwStageBytes;
     Barriers* bars = reinterpret_cast<Barriers*>(staging0 + kDwStagingBytes);
     const Tables tab(reinterpret_cast<uint8_t*>(bars) + kBarBytes, s.experts);
-    volatile int* abort = &bars->abort;
+    volatile int *abort = &bars->abort, *begun = &bars->begun;
     const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // an expert without rows has a zero gradient: written, or nothing to add
@@ -552,6 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_load_2d_pair(sa + kDwHalfBytes + c * (kBK * 128), &tmap_x, bar,
                                          n0 + 64 * c, w.r0 + k0);
                     }
+                    *begun = it + 1;
                 }
             }
             if (*abort)  // let copies already issued land before the pair ends
@@ -572,7 +603,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             it += blocks;
             if (valid == 0) continue;
             const int st = (it - 1) % stages;
-            ok = warp_wait(&bars->landed[st], (tail_phases >> st) & 1, kSiteLanded, abort);
+            ok = __all_sync(0xffffffffu,
+                            wait_landed(&bars->landed[st], (tail_phases >> st) & 1, begun, abort));
             if (!ok) break;
             tail_phases ^= 1u << st;
             clear_rows(smem + st * kDwStageBytes, valid, lane);

@@ -138,6 +138,23 @@ def test_grouped_products_just_below_their_limit():
         assert ((dw[e].double() - ref).abs() <= bound).all()
 
 
+def test_the_longest_reduction_there_may_be():
+    """One expert with 2^28 - 1 rows, the last 63 of them a tail, behind which nothing is left to
+    do: 4 million k-blocks on one pair of SMs.  Partial sums of n chunks grow like sqrt(k) and are
+    rounded to nearest: u sqrt(n / 6) = 1.8e-5 relative, beside 1.3e-6 within the chunks; four
+    times their sum bounds the norm of 64 such errors."""
+    rows, f = 2 ** 28 - 1, 8
+    x, dy = normal((rows, f), 1, torch.bfloat16), normal((rows, f), 2, torch.bfloat16)
+    off = torch.tensor([0, 0, rows], dtype=torch.int32, device=DEV)
+    dw = fa.linear_grouped_bwd_dw(dy, x, off)
+    fa.check_device_error()
+    ref = torch.zeros((f, f), dtype=torch.float64, device=DEV)
+    for r in range(0, rows, 1 << 23):
+        ref += dy[r:r + (1 << 23)].double().t() @ x[r:r + (1 << 23)].double()
+    assert not dw[0].any()
+    assert (dw[1].double() - ref).norm() <= 8e-5 * ref.norm()
+
+
 def test_a_gradient_of_more_than_2_31_values():
     n = 2 ** 31 + 12345
     big, small = torch.full((n,), 0.25, dtype=torch.float16, device=DEV), torch.ones(7, device=DEV)
