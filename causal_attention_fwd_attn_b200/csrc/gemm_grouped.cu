@@ -276,7 +276,7 @@ template <int BN, bool W_MN, bool OUT32, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ TokenMaps tmap_x,
-                        const int* __restrict__ offsets, void* __restrict__ out, const RowsShape s) {
+                        const int* offsets, void* out, const RowsShape s) {
     using C = RowsCfg<BN, OUT32>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -532,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_dw_kernel(const __grid_constant__ CUtensorMap tmap_dy,
                       const __grid_constant__ CUtensorMap tmap_x,
                       const __grid_constant__ CUtensorMap tmap_dw,
-                      const int* __restrict__ offsets, const DwShape s) {
+                      const int* offsets, const DwShape s) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -127,11 +127,11 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long e0, lon
         uint4 u[kFly];
 #pragma unroll
         for (int j = 0; j < kFly; ++j)
-            u[j] = KEEP ? __ldg(v + k + j * kThreads) : __ldcs(v + k + j * kThreads);
+            u[j] = KEEP ? v[k + j * kThreads] : __ldcs(v + k + j * kThreads);
 #pragma unroll
         for (int j = 0; j < kFly; ++j) take(u[j], acc[j % 4]);
     }
-    for (; k < n; k += kThreads) take(__ldg(v + k), acc[0]);
+    for (; k < n; k += kThreads) take(v[k], acc[0]);
     float tail = 0.f;
     const long long e = e0 + (long long)n * P + threadIdx.x;
     if (e < e1) {
@@ -147,7 +147,7 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long e0, lon
     double s = (double)tail * (double)tail;
     for (int q = threadIdx.x; q < n; q += kThreads) {
         float f[P];
-        values<DT>(__ldg(v + q), f);
+        values<DT>(v[q], f);
 #pragma unroll
         for (int j = 0; j < P; ++j) s = fma((double)f[j], (double)f[j], s);
     }
@@ -163,7 +163,7 @@ __device__ __forceinline__ double squares(int dtype, const void* g, long long e0
 
 // Chunks from `keep` on stay in L2.
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    grad_norm_kernel(const __grid_constant__ Table t, double* __restrict__ partials, int keep) {
+    grad_norm_kernel(const __grid_constant__ Table t, double* partials, int keep) {
     allow_dependents_launch();
     grid_dependency_wait();
     const int chunks = t.chunk0[t.count];
@@ -187,7 +187,7 @@ __device__ __forceinline__ double norm_of(const double* partials, int n) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-    grad_norm_sum_kernel(const double* __restrict__ partials, int n, float* norm_out) {
+    grad_norm_sum_kernel(const double* partials, int n, float* norm_out) {
     allow_dependents_launch();
     grid_dependency_wait();
     const double norm = norm_of(partials, n);
@@ -239,7 +239,7 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long 
 }
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    grad_clip_kernel(const __grid_constant__ Table t, const double* __restrict__ partials, int n,
+    grad_clip_kernel(const __grid_constant__ Table t, const double* partials, int n,
                      float max_norm, float* norm_out) {
     allow_dependents_launch();
     grid_dependency_wait();

@@ -127,8 +127,8 @@ __device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsig
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const int j = lane_id() + 32 * m;
-        ax[m] = r.axis && j < r.pairs ? min(max(__ldg(r.axis + j), 0), r.axes - 1) : 0;
-        f[m] = j < r.pairs ? __ldg(r.freq + j) : 0.0;
+        ax[m] = r.axis && j < r.pairs ? min(max(r.axis[j], 0), r.axes - 1) : 0;
+        f[m] = j < r.pairs ? r.freq[j] : 0.0;
     }
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -138,7 +138,7 @@ __device__ __forceinline__ void fill_angles(const Rope& r, const Shape& s, unsig
             on[n][m] = (int)lane_id() + 32 * m < r.pairs && tok < s.tokens;
             int p = 0;
             if (on[n][m])
-                p = r.pos ? __ldg(r.pos + (size_t)ax[m] * s.tokens + tok)
+                p = r.pos ? r.pos[(size_t)ax[m] * s.tokens + tok]
                           : (int)(tok % (unsigned)s.T);
             turns[n][m] = (double)p;
         }
@@ -480,7 +480,7 @@ struct Bwd {
 template <int D, bool F16, bool G32, bool ADJ>
 __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
     qkv_bwd_kernel(const __grid_constant__ Parts parts, const Rope rope, const Shape s, int nq, int nk,
-                   int per, float* __restrict__ partials) {
+                   int per, float* partials) {
     using C = Cfg<D>;
     using R = Bwd<G32>;
     constexpr int L = C::kLanes, kTok = C::kTok;
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<G32>::kBlocksPerSm)
 // elements; block y: q or k (partials [first, first + n)).
 constexpr int kSumRows = 128;
 __global__ void __launch_bounds__(8 * kSumRows)
-    qkv_dw_kernel(const float* __restrict__ partials, float* dwq, float* dwk, int nq, int nk, int D,
+    qkv_dw_kernel(const float* partials, float* dwq, float* dwk, int nq, int nk, int D,
                   int accumulate) {
     allow_dependents_launch();
     grid_dependency_wait();
