@@ -703,6 +703,12 @@ __global__ void __launch_bounds__(8 * kSumRows)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Two ranges of `n` bytes.
+bool overlap(const void* a, const void* b, long long n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)n && y < x + (uintptr_t)n;
+}
+
 // A gradient tensor's rows must not overlap: each stride (of a dimension longer than one)
 // at least the extent of the dimensions inside it.
 bool distinct(const forge_qkv_tensor& t, int B, int T, int heads, int d) {
@@ -860,6 +866,10 @@ int forge_qkv_fwd(const forge_qkv_config* c, const forge_qkv_tensor* q, const fo
         if ((st = check_strides(*in[j], c->B, c->T, heads[j])) != FORGE_ATTN_OK) return st;
         if (!aligned(out[j], 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
+    for (int j = 0; j < 3; ++j)
+        if (out[j] && out[(j + 1) % 3] &&
+            overlap(out[j], out[(j + 1) % 3], 2ll * c->B * c->T * c->H * c->d))
+            return FORGE_ATTN_ERR_INVALID_ARG;
     const long long tokens = (long long)c->B * c->T, tok = c->d == 64 ? Cfg<64>::kTok : Cfg<128>::kTok,
                     tiles = (tokens + tok - 1) / tok;
     Parts parts;
@@ -941,6 +951,9 @@ int forge_qkv_bwd(const forge_qkv_config* c, const void* dq, const void* dk, con
             return FORGE_ATTN_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return FORGE_ATTN_ERR_MISALIGNED;
     }
+    // (each is read, added to and written by its own blocks of the second kernel)
+    if (out[0] && weight[0] && out[1] && weight[1] && overlap(dw[0], dw[1], 4ll * c->d))
+        return FORGE_ATTN_ERR_INVALID_ARG;
     const bool f16 = (flags & FORGE_ATTN_FP16) != 0, g32 = (flags & FORGE_QKV_GRAD_F32) != 0;
     const long long tokens = (long long)c->B * c->T, tok = c->d == 64 ? Cfg<64>::kTok : Cfg<128>::kTok,
                     tiles = (tokens + tok - 1) / tok;

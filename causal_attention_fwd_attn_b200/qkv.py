@@ -21,7 +21,8 @@ def qkv_fwd(q, k, v, q_weight=None, k_weight=None, *, eps=1e-6, inv_freq=None, p
     inv_freq: float64 [rot / 2], the angle per position of each pair of the first rot
     elements (None: no rotation).  positions: int32 [B, T] or [axes, B, T] (None: 0 .. T - 1);
     pair_axis: int32 [rot / 2], the axis of each pair (None: axis 0).  Pairs are
-    (j, j + rot / 2), or with `adjacent` (2j, 2j + 1).  out: (q, k, v) to write into."""
+    (j, j + rot / 2), or with `adjacent` (2j, 2j + 1).  out: (q, k, v) to write into, three
+    tensors that do not overlap."""
     return _lib.front().qkv_fwd(q, k, v, q_weight, k_weight, eps, inv_freq, positions, pair_axis,
                                 adjacent, out)
 
@@ -35,7 +36,8 @@ def qkv_bwd(dq, dk, dv, q, k, q_weight=None, k_weight=None, *, eps=1e-6, inv_fre
     dq, dk, dv: contiguous [B, H, T, d], in q's type or fp32 (as attn_bwd returns them); q, k
     and the other arguments as for qkv_fwd.  out: (q, k, v) views to write into (default:
     slices of one packed [B, T, H + 2 Hkv, d] tensor).  weight_out: (q_weight, k_weight) to
-    write into, or to add to with `accumulate`.  workspace: uint8 of at least
+    write into, or to add to with `accumulate`; two tensors, also where q and k share one
+    weight (whose gradient is their sum).  workspace: uint8 of at least
     qkv_workspace_bytes(d)."""
     return _lib.front().qkv_bwd(dq, dk, dv, q, k, q_weight, k_weight, eps, inv_freq, positions,
                                 pair_axis, adjacent, out, weight_out, accumulate, workspace)

@@ -265,7 +265,8 @@ typedef struct {
 /*
  * Forward.  q, k, v: the projection's tensors (H, Hkv and Hkv heads), bf16 or fp16 with
  * FORGE_ATTN_FP16; q_out, k_out, v_out: contiguous [B][H][T][d] of the same type, as
- * forge_attn_fwd reads them.  A tensor and its output may both be NULL (left out).
+ * forge_attn_fwd reads them, overlapping neither the inputs nor each other (the latter is
+ * checked).  A tensor and its output may both be NULL (left out).
  * B * T * H * d < 2^31.  One launch; deterministic.  flags: FORGE_ATTN_FP16,
  * FORGE_QKV_ADJACENT.
  */
@@ -283,8 +284,9 @@ size_t forge_qkv_bwd_workspace_size(int d);
  * only where their weight is given, else they may be NULL).  q_grad, k_grad, v_grad: where
  * the projection's gradients go, 16-bit, laid out like its tensors; their elements must not
  * coincide (checked within each tensor).  A gradient and its output may both be NULL.
- * dq_weight, dk_weight: fp32 [d], required where the weight is given; accumulate = 1 adds
- * to their contents.  The gradients of shared key / value heads are summed in fp32 before
+ * dq_weight, dk_weight: fp32 [d], required where the weight is given, not overlapping (where q
+ * and k share one weight, its gradient is the sum of the two); accumulate = 1 adds to their
+ * contents.  The gradients of shared key / value heads are summed in fp32 before
  * anything is rounded.  One launch, and a small second one where a norm weight is given;
  * deterministic (no atomics).  workspace: 16-byte aligned, contents unspecified on entry and
  * on return.  flags: FORGE_ATTN_FP16, FORGE_QKV_ADJACENT, FORGE_QKV_GRAD_F32.

@@ -99,6 +99,31 @@ def test_qkv_backward_rejects_bad_arguments():
                               P, ws, 0, None) == _lib.ERR_INVALID_ARG
 
 
+def test_qkv_rejects_outputs_that_overlap():
+    """The same tensor twice, or neighbours that share their ends."""
+    size = 2 * 2 * 5 * 4 * 64  # bytes of an output
+    far = [P + n * (size + 16) for n in range(3)]
+    for outs in ((far[0], far[0], far[2]), (far[0], far[1], far[1]), (far[0], far[1], far[0]),
+                 (far[1] - 32, far[1], far[2]), (far[0], far[2] + 32, far[2])):
+        assert fwd(outs=outs) == _lib.ERR_INVALID_ARG
+    # far apart, nothing else is wrong: the launch itself fails without a device
+    if not torch.cuda.is_available():
+        assert fwd(outs=far) == _lib.ERR_CUDA
+    # both weights' gradients: one would be lost
+    ws = _lib.forge_qkv_bwd_workspace_size(64)
+
+    def bwd(dq_weight, dk_weight, cfg=None):
+        return _lib.forge_qkv_bwd(cfg or config(), P, P, P, tensor(), tensor(), tensor(), tensor(), tensor(),
+                                  dq_weight, dk_weight, 1, P, ws, 0, None)
+
+    assert bwd(P, P) == _lib.ERR_INVALID_ARG
+    assert bwd(P, P + 252) == _lib.ERR_INVALID_ARG
+    assert bwd(P + 128, P) == _lib.ERR_INVALID_ARG
+    if not torch.cuda.is_available():
+        assert bwd(P, P + 256) == _lib.ERR_CUDA
+        assert bwd(P, P, config(k_weight=None)) == _lib.ERR_CUDA  # only one is written
+
+
 def test_grouped_rejects_bad_arguments():
     for fn in (_lib.forge_linear_grouped_fwd, _lib.forge_linear_grouped_bwd_dx):
         assert fn(P, P, P, P, 0, 4, 64, 64, 0, None) == _lib.OK  # no rows: nothing to do

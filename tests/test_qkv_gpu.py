@@ -433,3 +433,28 @@ def test_front_end_refusals_on_cuda_tensors():
     odd = torch.zeros(2 * 3 * 4 * 64 + 4, dtype=torch.bfloat16, device=DEV)[4:].view(2, 3, 4, 64)
     with pytest.raises(fa.ForgeAttnError, match="misaligned"):
         fa.qkv_fwd(odd, odd, odd)
+
+
+def test_overlapping_outputs_are_refused():
+    """What two parts of the kernel would both write: one of the results would be lost."""
+    B, T, H, d = 1, 70, 2, 64
+    x = torch.randn((B, T, H, d), device=DEV).to(torch.bfloat16)
+    w = torch.ones(d, device=DEV)
+    room = torch.zeros(4 * B * H * T * d, dtype=torch.bfloat16, device=DEV)
+    n = B * H * T * d
+    o = [room[j * n:(j + 1) * n].view(B, H, T, d) for j in range(3)]
+    late = room[2 * n - 8:3 * n - 8].view(B, H, T, d)
+    for out in ((o[0], o[0], o[2]), (o[0], o[1], o[0]), (o[0], o[1], late)):
+        with pytest.raises(fa.ForgeAttnError, match="invalid argument"):
+            fa.qkv_fwd(x, x, x, w, w, out=out)
+    assert not room.any()
+    want = fa.qkv_fwd(x, x, x, w, w)
+    assert all(torch.equal(a, b) for a, b in zip(want, fa.qkv_fwd(x, x, x, w, w, out=tuple(o))))
+    g = torch.randn((B, H, T, d), device=DEV)
+    both = torch.zeros(2 * d, device=DEV)
+    for dq, dk in ((both[:d], both[:d]), (both[:d], both[4:d + 4])):
+        with pytest.raises(fa.ForgeAttnError, match="invalid argument"):
+            fa.qkv_bwd(g, g, g, x, x, w, w, weight_out=(dq, dk), accumulate=True)
+    assert not both.any()
+    *_, gq, gk = fa.qkv_bwd(g, g, g, x, x, w, w, weight_out=(both[:d], both[d:]), accumulate=True)
+    assert torch.equal(gq, gk) and gq.any()
