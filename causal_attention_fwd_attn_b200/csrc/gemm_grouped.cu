@@ -18,11 +18,13 @@
 // the rows after the expert's end are cleared in shared memory, in both operands (a
 // neighbour's row may hold infinities, which a zero in one operand would not remove).
 //
-// Sums for fp32 outputs: a tensor core cuts the bits off that its accumulator has no room
-// for, an error that points towards zero and grows with the number of additions (2.8e-6
-// relative after 2048 terms, 2e-5 after 16384).  Reductions into fp32 outputs therefore leave
-// tensor memory every 512 terms and go on in registers, rounded to nearest (below 1e-6 at
-// any length).  16-bit outputs round at 2^-9 and more, and take the whole reduction at once.
+// Sums: a tensor core cuts the bits off that its accumulator has no room for, an error that
+// points towards zero and grows with the number of additions (2.8e-6 relative after 2048 terms of
+// both signs, 2e-5 after 16384; fp16 terms of one sign 2.8e-6 after 512, 6.9e-3 after 2^20).
+// Reductions therefore leave tensor memory in chunks and go on in fp32 registers, rounded to
+// nearest: every 512 terms for fp32 outputs (0.5e-6 for terms of both signs), every 4096 for 16-bit
+// ones, where what a chunk loses (256 additions, 2^-23 each at most: 3.1e-5 of its terms'
+// magnitudes) is small beside fp16's half step of 2^-11 and bf16's of 2^-8.
 //
 // What bounds them: copies into shared memory where an expert has many rows (a k-block of a
 // 256 x 256 tile brings 32 KB into each SM, 512 clocks at the 64 bytes a clock that L2 gives
@@ -54,7 +56,9 @@ constexpr int kThreads = 128 * (1 + kGroups);
 constexpr int kBK = 64;
 constexpr int kHalfM = 128;        // a block's rows of a pair's 256
 constexpr int kAccCols = 256;      // tensor memory columns of one of the two accumulators
-constexpr int kChunkBlocks = 8;    // k-blocks of a reduction's chunk for fp32 outputs
+// k-blocks of a reduction's chunk, after which its sums leave tensor memory: for fp32 outputs, and
+// for 16-bit ones (the forward of 16384 rows took 249 us with 8, 242 with 16, 240 with 64).
+constexpr int kChunk32 = 8, kChunk16 = 64;
 constexpr int kMaxStages = 10;
 constexpr int kMaxSmem = 232448;   // shared memory of a block
 
@@ -193,6 +197,7 @@ struct RowsCfg {
     static constexpr int kABytes = kHalfM * kBK * 2;
     static constexpr int kStageBytes = kABytes + BN / 2 * kBK * 2;
     static constexpr int kRowBytes = kHalfM * (OUT32 ? 4 : 2);
+    static constexpr int kChunk = OUT32 ? kChunk32 : kChunk16;
     // 32-token steps of an accumulator that a group of epilogue warps takes
     static constexpr int kSteps = BN / kStageRows / kGroups;
     static constexpr int kStagingBytes = kGroups * kStageRows * kRowBytes;
@@ -343,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const RowsUnit w = rows_unit(tab, most, u, e);
             const uint32_t idesc = kIdesc0 | ((uint32_t)(w.width >> 3) << 17);
             for (int kb0 = 0; ok && kb0 < s.k_blocks; ++n_acc) {
-                const int kb1 = OUT32 ? min(kb0 + kChunkBlocks, s.k_blocks) : s.k_blocks;
+                const int kb1 = min(kb0 + C::kChunk, s.k_blocks);
                 const int buf = n_acc & 1, use = n_acc >> 1;
                 if (use > 0 &&
                     !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
@@ -382,7 +387,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (quarter * 32u) << 16;
         const int tid = (int)threadIdx.x - 128 * (1 + (int)group);
         constexpr int kEl = OUT32 ? 4 : 2, kRowBytes = C::kRowBytes, kChunks = kRowBytes / 16;
-        constexpr int kKept = OUT32 ? 32 : 16;  // registers of a step: sums, or 16-bit pairs
         uint8_t* staging = staging0 + group * (kStageRows * kRowBytes);
         const uint32_t empty_bar[2] = {cluster_addr(&bars->acc_empty[0], 0),
                                        cluster_addr(&bars->acc_empty[1], 0)};
@@ -391,14 +395,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = pair; ok && u < units; u += pairs) {
             const RowsUnit w = rows_unit(tab, most, u, e);
             const int fm = w.fm + (int)rank * kHalfM;
-            uint32_t kept[C::kSteps][kKept];
-            if constexpr (OUT32) {
+            float sum[C::kSteps][kStageRows];
 #pragma unroll
-                for (int q = 0; q < C::kSteps; ++q)
+            for (int q = 0; q < C::kSteps; ++q)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) kept[q][j] = 0u;
-            }
-            const int chunks = OUT32 ? (s.k_blocks + kChunkBlocks - 1) / kChunkBlocks : 1;
+                for (int j = 0; j < kStageRows; ++j) sum[q][j] = 0.f;
+            const int chunks = (s.k_blocks + C::kChunk - 1) / C::kChunk;
             for (int c = 0; c < chunks; ++c, ++n_acc) {
                 const int buf = n_acc & 1;
                 // the group goes on, or gives up, together: it meets at barriers below
@@ -412,26 +414,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int c0 = (kGroups * q + (int)group) * kStageRows;
                     if (c0 >= w.width) break;
                     const uint32_t from = tmem + lane_off + buf * kAccCols + c0;
-                    if constexpr (OUT32) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t r[16];
-                            tmem_ld16(from + 16 * h, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                kept[q][16 * h + j] =
-                                    __float_as_uint(__uint_as_float(kept[q][16 * h + j]) +
-                                                    __uint_as_float(r[j]));
-                        }
-                    } else {
-                        uint32_t r[32];
-                        tmem_ld32(from, r);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[16];
+                        tmem_ld16(from + 16 * h, r);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            kept[q][j] = pack16x2<F16>(__uint_as_float(r[2 * j]),
-                                                       __uint_as_float(r[2 * j + 1]));
+                        for (int j = 0; j < 16; ++j) sum[q][16 * h + j] += __uint_as_float(r[j]);
                     }
                 }
                 tc_fence_before();
@@ -445,12 +434,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (c0 >= w.width) break;
                 named_barrier_sync(1 + group, 128);  // the staging rows have been read
 #pragma unroll
-                for (int j = 0; j < kStageRows; ++j) {
+                for (int j = 0; j < kStageRows; j += 2) {
                     uint8_t* dst = staging + j * kRowBytes + (quarter * 32 + lane) * kEl;
-                    if constexpr (OUT32) *reinterpret_cast<uint32_t*>(dst) = kept[q][j];
-                    else
-                        *reinterpret_cast<uint16_t*>(dst) =
-                            (uint16_t)(kept[q][j / 2] >> (j % 2 * 16));
+                    if constexpr (OUT32) {
+                        *reinterpret_cast<float*>(dst) = sum[q][j];
+                        *reinterpret_cast<float*>(dst + kRowBytes) = sum[q][j + 1];
+                    } else {
+                        const uint32_t two = pack16x2<F16>(sum[q][j], sum[q][j + 1]);
+                        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)two;
+                        *reinterpret_cast<uint16_t*>(dst + kRowBytes) = (uint16_t)(two >> 16);
+                    }
                 }
                 named_barrier_sync(1 + group, 128);
                 const int live = min(kStageRows, w.n - c0);
@@ -621,8 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
             const int blocks = (w.count + kBK - 1) / kBK;
-            for (int kb0 = 0; ok && kb0 < blocks; kb0 += kChunkBlocks, ++n_acc) {
-                const int kb1 = min(kb0 + kChunkBlocks, blocks);
+            for (int kb0 = 0; ok && kb0 < blocks; kb0 += kChunk32, ++n_acc) {
+                const int kb1 = min(kb0 + kChunk32, blocks);
                 const int buf = n_acc & 1, use = n_acc >> 1;
                 if (use > 0 &&
                     !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
@@ -665,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs) {
             const DwUnit w = dw_unit(tab, s, u, e);
-            const int chunks = (w.count + kChunkBlocks * kBK - 1) / (kChunkBlocks * kBK);
+            const int chunks = (w.count + kChunk32 * kBK - 1) / (kChunk32 * kBK);
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.f;

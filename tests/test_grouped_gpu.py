@@ -172,6 +172,33 @@ def test_long_reductions_keep_fp32s_precision():
     assert float((y - ref).norm() / ref.norm()) <= 1.3e-6
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K", [4096, 4104, 8192, 65536 + 8, 2 ** 20])
+def test_long_reductions_into_16_bit_outputs(K, dtype):
+    """Terms of one sign, the worst for sums that are cut off: in chunks of 4096 terms at most
+    4096 / 16 + 1 additions lose 2^-23 each, the chunks' sums lose 2^-24 each, and the output its
+    half step, of sums of magnitudes that are the values themselves.  (In one piece 2^20 terms lost
+    7e-3.)"""
+    g = torch.Generator(device=DEV).manual_seed(K)
+    a, w = ((torch.rand(s, generator=g, device=DEV) * 0.2).to(dtype) for s in ((40, K), (1, 72, K)))
+    off = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    ref = a.double() @ w[0].double().t()
+    assert ref.max() < 3e4
+    bound = HALF[dtype] + 2.0 ** -23 * (4096 / 16 + 1) + 2.0 ** -24 * (K / 4096)
+    y = fa.linear_grouped_fwd(a, w, off)
+    dx = fa.linear_grouped_bwd_dx(a, w.transpose(1, 2).contiguous(), off)
+    fa.check_device_error()
+    for got in (y, dx):
+        assert got.dtype == dtype
+        assert float(((got.double() - ref) / ref).abs().max()) <= bound
+
+
+def test_chunks_of_ragged_experts():
+    """Reductions of several chunks and a rest, over tiles of several widths, empty ones between."""
+    run([70, 5, 0, 300], 4104, 136, seed=41, what=("y",))
+    run([33, 0, 257], 72, 8264, seed=42, dtype=torch.float16, what=("dx",), first=3, spare=9)
+
+
 @pytest.mark.parametrize("rows", [130, 160, 190, 225, 250, 290, 330, 1000])
 def test_every_tile_width(rows):
     """One expert: the device's choice of the tile's width goes through its range."""
