@@ -195,10 +195,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // out = c g over elements [e0, e1).  In 16-bit types the product is rounded once, to
-// nearest; c = 1 copies the values.
-template <int DT>
+// nearest; c = 1 copies the values.  F: c in fp32, or in 64 bits where fp32 has no normal number
+// for it while the products may well be ordinary ones.
+template <int DT, typename F>
 __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long e0, long long e1,
-                                            float c) {
+                                            F c) {
     constexpr int P = kPer<DT>;
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(g) + e0 * (16 / P));
     uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + e0 * (16 / P));
@@ -207,7 +208,7 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long 
         float f[P];
         values<DT>(u, f);
 #pragma unroll
-        for (int j = 0; j < P; ++j) f[j] *= c;
+        for (int j = 0; j < P; ++j) f[j] = (float)(f[j] * c);
         uint4 r;
         if constexpr (DT == FORGE_GRAD_F32) {
             r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
@@ -230,12 +231,20 @@ __device__ __forceinline__ void chunk_scale(const void* g, void* out, long long 
     for (; k < n; k += kThreads) put(k, __ldcs(v + k));
     const long long e = e0 + (long long)n * P + threadIdx.x;
     if (e < e1) {
-        const float r = value<DT>(g, e) * c;
+        const float r = (float)(value<DT>(g, e) * c);
         if constexpr (DT == FORGE_GRAD_F32) static_cast<float*>(out)[e] = r;
         else if constexpr (DT == FORGE_GRAD_BF16)
             static_cast<__nv_bfloat16*>(out)[e] = __float2bfloat16_rn(r);
         else static_cast<__half*>(out)[e] = __float2half_rn(r);
     }
+}
+
+template <typename F>
+__device__ __forceinline__ void scale(int dtype, const void* g, void* out, long long e0, long long e1,
+                                      F c) {
+    if (dtype == FORGE_GRAD_F32) chunk_scale<FORGE_GRAD_F32>(g, out, e0, e1, c);
+    else if (dtype == FORGE_GRAD_BF16) chunk_scale<FORGE_GRAD_BF16>(g, out, e0, e1, c);
+    else chunk_scale<FORGE_GRAD_F16>(g, out, e0, e1, c);
 }
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
@@ -245,17 +254,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grid_dependency_wait();
     const double norm = norm_of(partials, n);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    const float c = norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+    const double wide = norm > (double)max_norm ? (double)max_norm / norm : 1.0;
+    const float c = (float)wide;
+    const bool tiny = wide < 0x1p-126 && wide > 0.0;  // (an infinite norm makes it 0)
     for (int ch = t.chunk0[t.count] - 1 - (int)blockIdx.x; ch >= 0; ch -= (int)gridDim.x) {
         const int i = tensor_of(t, ch);
         if (c == 1.f && t.out[i] == t.grad[i]) continue;  // nothing to change in place
         const long long e0 = (long long)(ch - t.chunk0[i]) * t.chunk;
         const long long e1 = min(e0 + t.chunk, t.n[i]);
-        if (t.dtype[i] == FORGE_GRAD_F32)
-            chunk_scale<FORGE_GRAD_F32>(t.grad[i], t.out[i], e0, e1, c);
-        else if (t.dtype[i] == FORGE_GRAD_BF16)
-            chunk_scale<FORGE_GRAD_BF16>(t.grad[i], t.out[i], e0, e1, c);
-        else chunk_scale<FORGE_GRAD_F16>(t.grad[i], t.out[i], e0, e1, c);
+        if (tiny) scale(t.dtype[i], t.grad[i], t.out[i], e0, e1, wide);
+        else scale(t.dtype[i], t.grad[i], t.out[i], e0, e1, c);
     }
 }
 

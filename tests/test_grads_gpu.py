@@ -105,6 +105,19 @@ def test_squares_beyond_fp32s_range():
     assert fa.grad_norm([torch.zeros(9000, device=DEV), -torch.zeros(9, device=DEV)]).item() == 0.0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_factors_below_fp32s_normal_range(in_place):
+    """max_norm / norm down to 1e-60 while the clipped values are ordinary: the factor keeps its
+    bits (in fp32 it would be 0.05 % to 2 % off, or 0)."""
+    for n, top, max_norm in ((5000, 3e38, 1e-3), (5000, 3e38, 1e-20), (70001, 3.3e38, 1e-2),
+                             (40, 2e38, 1.0)):
+        for kinds in (KINDS[:1], KINDS[1:2], KINDS):
+            grads = [t.abs().add(0.1).mul(top / 10).to(t.dtype) if t.dtype != torch.float16 else t
+                     for t in make([n, 333, 5], kinds, n, sigma=1.0)]
+            assert all(torch.isfinite(t).all() for t in grads)
+            check(grads, max_norm, in_place)
+
+
 def test_values_that_are_not_finite():
     grads = make([5000, 300], KINDS, 9)
     grads[1][17] = float("inf")
