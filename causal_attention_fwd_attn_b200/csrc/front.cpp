@@ -2,6 +2,9 @@
 // module: checks of the tensors' type, shape, layout and device, allocation of outputs, and
 // the call of the C ABI on the device's current stream.  No arithmetic happens here.
 //
+// Checks run with the interpreter's lock; allocations, which may wait for the device, and launches,
+// which wait where a stream's queue is full, run without it, so that other Python threads go on.
+//
 // On a few rows these operators take the GPU a few microseconds.  The same checks written in
 // Python cost the host 8 to 30 us a call (a dozen tensors, five attributes each) and would be
 // all that a decoding step waits for; here they cost well under one.
@@ -86,16 +89,42 @@ PyObject* wrap(Tensor t) {
     return o;
 }
 
-// A tuple or list of `n` items.
-struct Items {
-    PyObject* fast;
-    Items(PyObject* o, const char* what) : fast(PySequence_Fast(o, what)) {
-        if (!fast) throw PythonError{};
+// A reference of our own.
+struct Owned {
+    PyObject* o;
+    explicit Owned(PyObject* p) : o(p) {
+        if (!o) throw PythonError{};
     }
-    ~Items() { Py_XDECREF(fast); }
+    ~Owned() { Py_XDECREF(o); }
+    Owned(const Owned&) = delete;
+    PyObject* release() {
+        PyObject* p = o;
+        o = nullptr;
+        return p;
+    }
+};
+
+// The items of a sequence, held: a list that another thread changes meanwhile does not matter.
+struct Items {
+    PyObject* tuple;
+    Items(PyObject* o, const char* what) {
+        const Owned fast(PySequence_Fast(o, what));
+        tuple = PySequence_Tuple(fast.o);
+        if (!tuple) throw PythonError{};
+    }
+    ~Items() { Py_DECREF(tuple); }
     Items(const Items&) = delete;
-    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast); }
-    PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
+    Py_ssize_t size() const { return PyTuple_GET_SIZE(tuple); }
+    PyObject* operator[](Py_ssize_t i) const { return PyTuple_GET_ITEM(tuple, i); }
+};
+
+// Lets other Python threads run while it lives; nothing in its scope touches a Python object.  The
+// tensors that a call was given are held by its caller, or by Items.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+    Unlocked(const Unlocked&) = delete;
 };
 
 bool truth(PyObject* o) {
@@ -249,32 +278,31 @@ PyObject* qkv_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const char* names[3] = {"out q", "out k", "out v"};
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)s.index);
         void* out[3];
-        PyObject* result = PyTuple_New(3);
-        if (!result) throw PythonError{};
-        try {
-            if (given(a[10])) {
-                const Items items(a[10], "out must be (q, k, v)");
-                if (items.size() != 3) refuse("out must be (q, k, v)");
-                for (int j = 0; j < 3; ++j) {
-                    out[j] = check(tensor(items[j], names[j]), names[j], {s.type}, s.index, &shape);
-                    Py_INCREF(items[j]);
-                    PyTuple_SET_ITEM(result, j, items[j]);
-                }
-            } else {
-                for (int j = 0; j < 3; ++j) {
-                    Tensor t = empty(shape, s.type, s.index);
-                    out[j] = t.data_ptr();
-                    PyTuple_SET_ITEM(result, j, wrap(std::move(t)));
-                }
+        Tensor made[3];
+        Owned result(PyTuple_New(3));
+        const bool own = !given(a[10]);
+        if (!own) {
+            const Items items(a[10], "out must be (q, k, v)");
+            if (items.size() != 3) refuse("out must be (q, k, v)");
+            for (int j = 0; j < 3; ++j) {
+                out[j] = check(tensor(items[j], names[j]), names[j], {s.type}, s.index, &shape);
+                Py_INCREF(items[j]);
+                PyTuple_SET_ITEM(result.o, j, items[j]);
             }
-            done(forge_qkv_fwd(&s.config, &s.q, &s.k, &v, out[0], out[1], out[2], s.flags,
-                               stream_of(s.index)),
-                 "forge_qkv_fwd");
-        } catch (...) {
-            Py_DECREF(result);
-            throw;
         }
-        return result;
+        int status;
+        {
+            const Unlocked unlocked;
+            for (int j = 0; own && j < 3; ++j) {
+                made[j] = empty(shape, s.type, s.index);
+                out[j] = made[j].data_ptr();
+            }
+            status = forge_qkv_fwd(&s.config, &s.q, &s.k, &v, out[0], out[1], out[2], s.flags,
+                                   stream_of(s.index));
+        }
+        done(status, "forge_qkv_fwd");
+        for (int j = 0; own && j < 3; ++j) PyTuple_SET_ITEM(result.o, j, wrap(std::move(made[j])));
+        return result.release();
     });
 }
 
@@ -300,70 +328,71 @@ PyObject* qkv_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)s.index);
         forge_qkv_tensor out[3];
         float* dw[2] = {nullptr, nullptr};
-        PyObject* result = PyTuple_New(5);
-        if (!result) throw PythonError{};
-        try {
-            if (given(a[12])) {
-                const Items items(a[12], "out must be (q, k, v)");
-                if (items.size() != 3) refuse("out must be (q, k, v)");
-                for (int j = 0; j < 3; ++j) {
-                    out[j] = view(tensor(items[j], names[j]), names[j], s, heads[j]);
-                    Py_INCREF(items[j]);
-                    PyTuple_SET_ITEM(result, j, items[j]);
-                }
-            } else {
+        Owned result(PyTuple_New(5));
+        auto keep = [&](int at, PyObject* o) {
+            Py_INCREF(o);
+            PyTuple_SET_ITEM(result.o, at, o);
+        };
+        const bool own = !given(a[12]);
+        if (!own) {
+            const Items items(a[12], "out must be (q, k, v)");
+            if (items.size() != 3) refuse("out must be (q, k, v)");
+            for (int j = 0; j < 3; ++j) {
+                out[j] = view(tensor(items[j], names[j]), names[j], s, heads[j]);
+                keep(j, items[j]);
+            }
+        }
+        const at::IntArrayRef head(&s.d, 1);
+        const float* weights[2] = {s.config.q_weight, s.config.k_weight};
+        bool own_dw[2] = {weights[0] != nullptr, weights[1] != nullptr};
+        for (int j = 0; j < 2; ++j)
+            if (!own_dw[j]) keep(3 + j, Py_None);
+        if (given(a[13])) {
+            const Items items(a[13], "weight_out must be (q_weight, k_weight)");
+            if (items.size() != 2) refuse("weight_out must be (q_weight, k_weight)");
+            for (int j = 0; j < 2; ++j) {
+                if (!own_dw[j] || !given(items[j])) continue;
+                dw[j] = (float*)check(tensor(items[j], "weight_out"), "weight_out", {kF32}, s.index,
+                                      &head);
+                own_dw[j] = false;
+                keep(3 + j, items[j]);
+            }
+        }
+        if (accumulate && (own_dw[0] || own_dw[1])) refuse("accumulate needs weight_out");
+        Tensor ws, made[3], made_dw[2];
+        if (given(a[15])) {
+            ws = tensor(a[15], "workspace");
+            check(ws, "workspace", {kU8}, s.index);
+        }
+        int status;
+        {
+            const Unlocked unlocked;
+            if (own) {
                 const Tensor packed = empty({s.B, s.T, s.H + 2 * s.Hkv, s.d}, s.type, s.index);
                 int64_t first = 0;
                 for (int j = 0; j < 3; ++j) {
-                    Tensor t = packed.narrow(2, first, heads[j]);
+                    made[j] = packed.narrow(2, first, heads[j]);
                     first += heads[j];
-                    out[j] = view(t, names[j], s, heads[j]);
-                    PyTuple_SET_ITEM(result, j, wrap(std::move(t)));
+                    out[j] = view(made[j], names[j], s, heads[j]);
                 }
             }
-            PyObject* kept[2] = {Py_None, Py_None};
-            std::unique_ptr<Items> items;  // holds what `kept` points to
-            if (given(a[13])) {
-                items = std::make_unique<Items>(a[13], "weight_out must be (q_weight, k_weight)");
-                if (items->size() != 2) refuse("weight_out must be (q_weight, k_weight)");
-                kept[0] = (*items)[0];
-                kept[1] = (*items)[1];
-            }
-            const at::IntArrayRef head(&s.d, 1);
-            const float* weights[2] = {s.config.q_weight, s.config.k_weight};
             for (int j = 0; j < 2; ++j) {
-                PyObject* o = Py_None;
-                if (!weights[j]) {
-                    Py_INCREF(o);
-                } else if (given(kept[j])) {
-                    dw[j] = (float*)check(tensor(kept[j], "weight_out"), "weight_out", {kF32}, s.index,
-                                          &head);
-                    o = kept[j];
-                    Py_INCREF(o);
-                } else {
-                    if (accumulate) refuse("accumulate needs weight_out");
-                    Tensor t = empty(head, kF32, s.index);
-                    dw[j] = t.data_ptr<float>();
-                    o = wrap(std::move(t));
-                }
-                PyTuple_SET_ITEM(result, 3 + j, o);
+                if (!own_dw[j]) continue;
+                made_dw[j] = empty(head, kF32, s.index);
+                dw[j] = made_dw[j].data_ptr<float>();
             }
-            Tensor ws;
-            if (given(a[15])) {
-                ws = tensor(a[15], "workspace");
-                check(ws, "workspace", {kU8}, s.index);
-            } else if (norm) {
+            if (!ws.defined() && norm)
                 ws = empty({(int64_t)forge_qkv_bwd_workspace_size(s.config.d)}, kU8, s.index);
-            }
-            done(forge_qkv_bwd(&s.config, dy[0], dy[1], dy[2], &s.q, &s.k, &out[0], &out[1], &out[2],
-                               dw[0], dw[1], accumulate, ws.defined() ? ws.data_ptr() : nullptr,
-                               ws.defined() ? (size_t)ws.numel() : 0, s.flags, stream_of(s.index)),
-                 "forge_qkv_bwd");
-        } catch (...) {
-            Py_DECREF(result);
-            throw;
+            status = forge_qkv_bwd(&s.config, dy[0], dy[1], dy[2], &s.q, &s.k, &out[0], &out[1],
+                                   &out[2], dw[0], dw[1], accumulate,
+                                   ws.defined() ? ws.data_ptr() : nullptr,
+                                   ws.defined() ? (size_t)ws.numel() : 0, s.flags, stream_of(s.index));
         }
-        return result;
+        done(status, "forge_qkv_bwd");
+        for (int j = 0; own && j < 3; ++j) PyTuple_SET_ITEM(result.o, j, wrap(std::move(made[j])));
+        for (int j = 0; j < 2; ++j)
+            if (own_dw[j]) PyTuple_SET_ITEM(result.o, 3 + j, wrap(std::move(made_dw[j])));
+        return result.release();
     });
 }
 
@@ -410,24 +439,27 @@ PyObject* grouped_rows(PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef shape(dims, 2);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
     Tensor y;
-    if (given(a[3])) {
+    const bool own = !given(a[3]);
+    const bool f32 = given(a[4]) && truth(a[4]);
+    if (!own) {
         y = tensor(a[3], "out");
         check(y, "out", {p.a.scalar_type(), kF32}, p.index, &shape);
-        if (given(a[4]) && truth(a[4]) != (y.scalar_type() == kF32))
-            refuse("out and out_dtype differ");
-    } else {
-        y = empty(shape, given(a[4]) && truth(a[4]) ? kF32 : p.a.scalar_type(), p.index);
+        if (given(a[4]) && f32 != (y.scalar_type() == kF32)) refuse("out and out_dtype differ");
     }
-    const int flags = p.flags | (y.scalar_type() == kF32 ? FORGE_ATTN_OUT_F32 : 0);
-    done((DX ? forge_linear_grouped_bwd_dx : forge_linear_grouped_fwd)(
-             p.a.data_ptr(), p.b.data_ptr(), y.data_ptr(), p.offsets, small(rows), small(experts),
-             small(fin), small(fout), flags, stream_of(p.index)),
-         DX ? "forge_linear_grouped_bwd_dx" : "forge_linear_grouped_fwd");
-    if (given(a[3])) {
-        Py_INCREF(a[3]);
-        return a[3];
+    const int n_rows = small(rows), n_experts = small(experts), n_in = small(fin), n_out = small(fout);
+    int status;
+    {
+        const Unlocked unlocked;
+        if (own) y = empty(shape, f32 ? kF32 : p.a.scalar_type(), p.index);
+        const int flags = p.flags | (y.scalar_type() == kF32 ? FORGE_ATTN_OUT_F32 : 0);
+        status = (DX ? forge_linear_grouped_bwd_dx : forge_linear_grouped_fwd)(
+            p.a.data_ptr(), p.b.data_ptr(), y.data_ptr(), p.offsets, n_rows, n_experts, n_in, n_out,
+            flags, stream_of(p.index));
     }
-    return wrap(std::move(y));
+    done(status, DX ? "forge_linear_grouped_bwd_dx" : "forge_linear_grouped_fwd");
+    if (own) return wrap(std::move(y));
+    Py_INCREF(a[3]);
+    return a[3];
 }
 PyObject* grouped_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] { return grouped_rows<false>(a, n); });
@@ -449,22 +481,27 @@ PyObject* grouped_dw(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::IntArrayRef shape(dims, 3);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
         Tensor dw;
-        if (given(a[3])) {
+        const bool own = !given(a[3]);
+        if (!own) {
             dw = tensor(a[3], "out");
             check(dw, "out", {kF32}, p.index, &shape);
-        } else {
-            if (accumulate) refuse("accumulate needs out");
-            dw = empty(shape, kF32, p.index);
+        } else if (accumulate) {
+            refuse("accumulate needs out");
         }
-        done(forge_linear_grouped_bwd_dw(p.a.data_ptr(), p.b.data_ptr(), (float*)dw.data_ptr(),
-                                         p.offsets, small(rows), small(p.experts), small(fin),
-                                         small(fout), accumulate, p.flags, stream_of(p.index)),
-             "forge_linear_grouped_bwd_dw");
-        if (given(a[3])) {
-            Py_INCREF(a[3]);
-            return a[3];
+        const int n_rows = small(rows), n_experts = small(p.experts), n_in = small(fin),
+                  n_out = small(fout);
+        int status;
+        {
+            const Unlocked unlocked;
+            if (own) dw = empty(shape, kF32, p.index);
+            status = forge_linear_grouped_bwd_dw(p.a.data_ptr(), p.b.data_ptr(), (float*)dw.data_ptr(),
+                                                 p.offsets, n_rows, n_experts, n_in, n_out, accumulate,
+                                                 p.flags, stream_of(p.index));
         }
-        return wrap(std::move(dw));
+        done(status, "forge_linear_grouped_bwd_dw");
+        if (own) return wrap(std::move(dw));
+        Py_INCREF(a[3]);
+        return a[3];
     });
 }
 
@@ -528,6 +565,7 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             refuse("gradients must be tensors on a CUDA device (there is no CPU path)");
         const int index = THPVariable_Unpack(grads[0]).get_device();
         const bool clip = truth(a[1]);
+        const float max_norm = clip ? (float)number(a[2]) : 0.f;
         std::vector<forge_grad_tensor> table((size_t)n);
         for (Py_ssize_t k = 0; k < n; ++k) {
             const Tensor& t = flat(grads[k], index, "gradients");
@@ -553,28 +591,27 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             norm = tensor(a[4], "norm");
             check(norm, "norm", {kF32}, index);
             if (norm.numel() != 1) refuse("norm must have one element");
-        } else {
-            norm = empty({}, kF32, index);
         }
         if (given(a[5])) {
             ws = tensor(a[5], "workspace");
             check(ws, "workspace", {kU8}, index);
-        } else {
-            ws = empty({(int64_t)forge_grad_workspace_size((int)n)}, kU8, index);
         }
-        if (clip)
-            done(forge_grad_clip(table.data(), (int)n, (float)number(a[2]), norm.data_ptr<float>(),
-                                 ws.data_ptr(), (size_t)ws.numel(), stream_of(index)),
-                 "forge_grad_clip");
-        else
-            done(forge_grad_norm(table.data(), (int)n, norm.data_ptr<float>(), ws.data_ptr(),
-                                 (size_t)ws.numel(), stream_of(index)),
-                 "forge_grad_norm");
-        if (given(a[4])) {
-            Py_INCREF(a[4]);
-            return a[4];
+        int status;
+        {
+            const Unlocked unlocked;
+            if (!norm.defined()) norm = empty({}, kF32, index);
+            if (!ws.defined()) ws = empty({(int64_t)forge_grad_workspace_size((int)n)}, kU8, index);
+            float* to = norm.data_ptr<float>();
+            const size_t bytes = (size_t)ws.numel();
+            status = clip ? forge_grad_clip(table.data(), (int)n, max_norm, to, ws.data_ptr(), bytes,
+                                            stream_of(index))
+                          : forge_grad_norm(table.data(), (int)n, to, ws.data_ptr(), bytes,
+                                            stream_of(index));
         }
-        return wrap(std::move(norm));
+        done(status, clip ? "forge_grad_clip" : "forge_grad_norm");
+        if (!given(a[4])) return wrap(std::move(norm));
+        Py_INCREF(a[4]);
+        return a[4];
     });
 }
 
