@@ -163,13 +163,17 @@ _front = None
 
 def front():
     """The native torch front end (csrc/front.cpp), loaded on the first call of one of its
-    functions.  Raises if it is not built."""
+    functions.  Raises if it is not built, or built for another torch or Python."""
     global _front
     if _front is None:
         load()
         if not os.path.exists(_build.FRONT):
             raise RuntimeError(f"the front end {_build.FRONT} is not built; run python -m "
                                "causal_attention_fwd_attn_b200.build")
+        built, here = _build.front_built_for(), _build.front_tag()
+        if built != here:
+            raise RuntimeError(f"the front end {_build.FRONT} was built for {built}, this is {here}; "
+                               "run python -m causal_attention_fwd_attn_b200.build")
         _front = importlib.import_module("._front", __package__)
     return _front
 

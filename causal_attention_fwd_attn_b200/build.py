@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import argparse
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -52,8 +53,32 @@ def _newer(target, files) -> bool:
     return all(os.path.getmtime(f) <= t for f in files)
 
 
+def front_tag() -> str:
+    """What the front end depends on beside its sources: it is compiled against the headers, and
+    so the object layouts, of one torch and one Python."""
+    import sysconfig
+
+    import torch
+
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def front_built_for():
+    """The tag that the built front end carries, without loading it; None if there is none."""
+    if not os.path.exists(FRONT):
+        return None
+    with open(FRONT, "rb") as f:
+        found = re.search(rb"forge front end built for ([^\0]*)\0", f.read())
+    return found.group(1).decode() if found else None
+
+
+def _front_current() -> bool:
+    return _newer(FRONT, [FRONT_SOURCE] + _headers()) and front_built_for() == front_tag()
+
+
 def up_to_date() -> bool:
-    return _newer(LIBRARY, _inputs()) and _newer(FRONT, [FRONT_SOURCE] + _headers())
+    return _newer(LIBRARY, _inputs()) and _front_current()
 
 
 def _build_front(verbose: bool) -> None:
@@ -69,7 +94,8 @@ def _build_front(verbose: bool) -> None:
                 sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
     cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DFORGE_FRONT_TAG="{front_tag()}"', "-I", INCLUDE]
     for p in includes:
         cmd += ["-isystem", p]
     cmd += [FRONT_SOURCE, "-o", FRONT + ".tmp", "-L", PKG, "-l:" + os.path.basename(LIBRARY),
@@ -103,7 +129,7 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     if force or ptxas_info or not _newer(LIBRARY, _inputs()):
         _run(cmd, "nvcc", verbose, show=ptxas_info)
         os.replace(LIBRARY + ".tmp", LIBRARY)
-    if force or not _newer(FRONT, [FRONT_SOURCE] + _headers()):
+    if force or not _front_current():
         _build_front(verbose)
     return LIBRARY
 

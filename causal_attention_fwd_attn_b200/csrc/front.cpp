@@ -28,6 +28,10 @@
 
 namespace {
 
+// Read from the file by build.py and _lib.py before this module is loaded: another torch's inline
+// accessors would read its tensors wrongly.
+[[gnu::used]] const char kTag[] = "forge front end built for " FORGE_FRONT_TAG;
+
 struct Refusal {  // becomes a ValueError
     std::string what;
 };
