@@ -6,6 +6,9 @@ end of the operators around the attention, a CPython module over it) in-tree.
 nvcc compiles for sm_100a only (tcgen05 and TMA need the arch-specific target);
 no GPU is needed to build.  ``--ptxas-info`` adds ``-Xptxas -v`` (registers,
 spills and shared memory per kernel).
+
+The library needs nvcc alone (run this file itself where torch is missing); without torch, or its
+headers or Python's, the front end is left out and the build says so.
 """
 from __future__ import annotations
 
@@ -53,6 +56,23 @@ def _newer(target, files) -> bool:
     return all(os.path.getmtime(f) <= t for f in files)
 
 
+def front_lacks():
+    """What is missing to build the front end, None if nothing is."""
+    import sysconfig
+
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    for what, path in (("torch's headers", os.path.join(root, "include", "ATen", "ATen.h")),
+                       ("torch with CUDA", os.path.join(root, "lib", "libc10_cuda.so")),
+                       ("Python's headers", os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
+        if not os.path.exists(path):
+            return f"{what} ({path})"
+    return None if shutil.which("g++") else "g++"
+
+
 def front_tag() -> str:
     """What the front end depends on beside its sources: it is compiled against the headers, and
     so the object layouts, of one torch and one Python."""
@@ -78,7 +98,7 @@ def _front_current() -> bool:
 
 
 def up_to_date() -> bool:
-    return _newer(LIBRARY, _inputs()) and _front_current()
+    return _newer(LIBRARY, _inputs()) and (front_lacks() is not None or _front_current())
 
 
 def _build_front(verbose: bool) -> None:
@@ -93,7 +113,7 @@ def _build_front(verbose: bool) -> None:
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
-    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+    cmd = [shutil.which("g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f'-DFORGE_FRONT_TAG="{front_tag()}"', "-I", INCLUDE]
     for p in includes:
@@ -129,7 +149,10 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     if force or ptxas_info or not _newer(LIBRARY, _inputs()):
         _run(cmd, "nvcc", verbose, show=ptxas_info)
         os.replace(LIBRARY + ".tmp", LIBRARY)
-    if force or not _front_current():
+    lacks = front_lacks()
+    if lacks is not None:
+        sys.stderr.write(f"{os.path.basename(FRONT)} is not built: no {lacks}\n")
+    elif force or not _front_current():
         _build_front(verbose)
     return LIBRARY
 
