@@ -46,3 +46,48 @@ def test_chains_of_small_calls_see_each_others_writes():
     want = chain(torch.cuda.synchronize)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(want, chain(lambda: None)))
+
+
+@pytest.mark.gpu
+def test_captured_between_memsets_copies_and_another_stream():
+    """In a graph the kernels' neighbours are nodes of other kinds, and several of them: replays
+    give what the same calls give eagerly."""
+    dev = torch.device("cuda", 0)
+    g = torch.Generator().manual_seed(5)
+
+    def rnd(*shape, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=g).to(dtype).to(dev)
+
+    x, w, rows, weights = rnd(1, 300, 2, 64), rnd(64, dtype=torch.float32), rnd(300, 128), rnd(3, 72, 128)
+    off = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device=dev)
+    none = torch.zeros(4, dtype=torch.int32, device=dev)
+    big = torch.zeros(300 * 128, dtype=torch.bfloat16, device=dev)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        big.zero_()  # a memset
+        q, k, v = fa.qkv_fwd(x, x, x, w, w)
+        big.copy_(rows.view(-1))  # a copy
+        side.wait_stream(here)
+        y = fa.linear_grouped_fwd(big.view(300, 128), weights, off)
+        with torch.cuda.stream(side):
+            gq, gk, gv, gwq, gwk = fa.qkv_bwd(q, k, v, x, x, w, w)
+        dw = fa.linear_grouped_bwd_dw(y, rows, off)
+        empty = fa.linear_grouped_bwd_dw(y[:0], rows[:0], none)  # a memset
+        here.wait_stream(side)  # two nodes ahead of the next kernel
+        norm = fa.grad_clip([dw, gwq, gwk, empty], 0.5)
+        return q, k, v, y, gq, gk, gv, gwq, gwk, dw, empty, norm
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(-3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    fa.check_device_error()
