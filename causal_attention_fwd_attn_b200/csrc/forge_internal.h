@@ -33,7 +33,11 @@ cudaError_t set_max_dynamic_smem(Kernel* kernel, int bytes,
 
 // Launches `kernel` with programmatic stream serialisation: its CTAs may be scheduled
 // while the previous kernel in the stream runs its last CTAs, and they wait in
-// grid_dependency_wait() (sm100_ptx.cuh) until that kernel has completed.
+// grid_dependency_wait() (sm100_ptx.cuh) until that kernel has completed.  What the kernel ahead
+// may write is not read-only for the lifetime of one that started beside it: kernels that let the
+// next one start before their own wait (qkv.cu, gemm_grouped.cu, grad.cu), so that more than two
+// may be resident, read it by ordinary loads (no __ldg, no const __restrict__), whose values the
+// wait makes visible.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t stream, Args&&... args) {

@@ -64,10 +64,7 @@ __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 // that kernel has completed and its memory writes are visible (immediately when the
 // launch had no such dependency); every thread calls it before touching global memory.
 // allow_dependents_launch() lets the next kernel of the stream be scheduled (it then
-// waits in its own grid_dependency_wait()).  What the kernel ahead may write is not read-only for
-// the lifetime of a kernel that started beside it: kernels that let the next one start before
-// their own wait (qkv.cu, gemm_grouped.cu, grad.cu), so that more than two may be resident, read
-// it by ordinary loads (no __ldg, no const __restrict__), whose values the wait makes visible.
+// waits in its own grid_dependency_wait()).
 __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
