@@ -26,12 +26,17 @@
 // ones, where what a chunk loses (256 additions, 2^-23 each at most: 3.1e-5 of its terms'
 // magnitudes) is small beside fp16's half step of 2^-11 and bf16's of 2^-8.
 //
-// What bounds them: copies into shared memory where an expert has many rows (a k-block of a
-// 256 x 256 tile brings 32 KB into each SM, 512 clocks at the 64 bytes a clock that L2 gives
-// it, as many as its products take; both at once take 700 to 770), the weights' HBM traffic where
-// few.  Forward of 16384 rows, 16 experts, 2048 -> 4096: 200 us, 1375 TFLOP/s (242 us once the power
-// limit has lowered the clock); of 32 rows, 20 of 32 experts: 58 us, 5.8 TB/s, 0.88 of the copy
-// rate.  dW of 16384 rows, 8 experts: 235 us, 1170 TFLOP/s (276).
+// What bounds them: the products and the copies that feed them where an expert has many rows (a
+// k-block of a 256 x 256 tile brings 32 KB into each SM, 512 clocks at the 64 bytes a clock that L2
+// gives it, as many as its products take; the forward takes 575 to 595 for it), the weights' HBM
+// traffic where few.  16384 rows of eight equal experts, 2048 -> 4096, in short bursts: forward
+// 184 us, 1490 TFLOP/s, dX 185; forward with fp32 outputs 210 (a chunk handed over every 512
+// terms, and twice the bytes stored); dW, which has the same chunks and outputs, 215.  Experts
+// whose rows are no multiple of 64 add 12 to dW (each unit's last copies wait for the rest to be
+// cleared), uneven ones as much again: units have their expert's length and are dealt in order, 480
+// k-blocks to the busiest pair against 450 on average: 236; accumulated 254.  Once the power limit
+// has lowered the clock the forward of 16 experts takes 242 (1137 TFLOP/s), dW 278.  32 rows, 20 of 32
+// experts: 58 us, 5.8 TB/s, 0.88 of the copy rate.
 //
 // Both are persistent, one block per SM.  Every block reads the offsets into shared
 // memory (each clamped to the rows there are, so that no offsets can lead outside the
@@ -104,12 +109,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, site, abort));
 }
 
-// Start of both kernels: barriers, tensor memory, tables; the pair begins together.
-// `full_count`: arrivals that a stage's products wait for.
-template <typename G, typename F>
-__device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
-                                      const int* offsets, int experts, int rows, G counted, F units_of);
-
 // Fills the tables: `units_of(rows)` units to an expert, asked after `counted()`, which the
 // whole block calls once the rows are known.  Ends with a barrier.
 template <typename G, typename F>
@@ -141,6 +140,8 @@ __device__ __forceinline__ void fill_tables(const Tables& t, const int* offsets,
     __syncthreads();
 }
 
+// Start of both kernels: barriers, tensor memory, tables; the pair begins together.
+// `full_count`: arrivals that a stage's products wait for.
 template <typename G, typename F>
 __device__ __forceinline__ void start(Barriers* bars, const Tables& tab, int stages, int full_count,
                                       const int* offsets, int experts, int rows, G counted, F units_of) {
@@ -215,7 +216,7 @@ struct RowsShape {
 };
 
 // A token matrix in boxes of 64 x 16 (n + 1): what a block copies of a product 32 (n + 1) wide,
-// no more (the copies are what paces the kernel).
+// no more.
 struct TokenMaps {
     CUtensorMap box[8];
 };
@@ -722,7 +723,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int check_dims(int rows, int experts, int in_f, int out_f) {
     if (rows < 0 || experts < 1 || in_f < 1 || out_f < 1) return FORGE_ATTN_ERR_INVALID_ARG;
     if (experts > kMaxExperts || in_f % 8 || out_f % 8) return FORGE_ATTN_ERR_UNSUPPORTED;
-    // (the longest reduction of one accumulator has to end well inside the limit of a wait)
+    // (the range that the sums' errors are stated and tested for)
     if (in_f > kMaxFeatures || out_f > kMaxFeatures) return FORGE_ATTN_ERR_UNSUPPORTED;
     if ((long long)rows * in_f >= (1ll << 31) || (long long)rows * out_f >= (1ll << 31) ||
         (long long)out_f * in_f >= (1ll << 31))
@@ -867,7 +868,7 @@ int forge_linear_grouped_bwd_dw(const void* dy, const void* x, float* dw, const 
         encode_map_2d16(&tb, x, in_features, rows, 64, kBK, f16) != cudaSuccess ||
         encode_map_3d(&td, dw, in_features, out_features, experts, 32, 32, kMapF32) != cudaSuccess)
         return FORGE_ATTN_ERR_CUDA;
-    const DwShape s{rows, experts, out_features, in_features, 
+    const DwShape s{rows, experts, out_features, in_features,
                     (out_features + 2 * kHalfM - 1) / (2 * kHalfM),
                     (in_features + 2 * kHalfM - 1) / (2 * kHalfM),
                     dw_stages(experts)};

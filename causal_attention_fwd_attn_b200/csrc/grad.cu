@@ -8,7 +8,7 @@
 // 16-bit ones.
 //
 // Both passes are bound by HBM: every value is read for the norm, and read and written
-// to be scaled (124.4M fp32 values: 76 us at 6.6 TB/s, and 168 us at 5.9; 244 together).  As in the AdamW step the tensor table travels in the kernel parameters
+// to be scaled (124.4M fp32 values: 76 us at 6.6 TB/s, and 168 us at 5.9; 246 together).  As in the AdamW step the tensor table travels in the kernel parameters
 // and the blocks of one grid walk fixed chunks of all tensors.  The norm pass leaves one
 // 64-bit partial per block; every block of the clip pass adds all of them itself, in the
 // same order, so that no counter, atomic or third launch is needed and the result does

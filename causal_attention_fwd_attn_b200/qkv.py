@@ -3,7 +3,9 @@
 keys, rotary positions with one or several axes, and the attention's head layout.
 
 The projection's tensors are [B, T, heads, d] views, usually slices of one packed
-[B, T, H + 2 Hkv, d] tensor; only the last dimension has to be contiguous.  The checks, the
+[B, T, H + 2 Hkv, d] tensor; only the last dimension has to be contiguous.  T may be 1 (a
+decoding step's tokens at positions of their own); attn_fwd reads q, k and v of one length and no
+cache, so that where such k and v go is the caller's.  The checks, the
 allocation and the call are in csrc/front.cpp.
 """
 from __future__ import annotations

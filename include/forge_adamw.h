@@ -78,10 +78,14 @@ int forge_adamw_step(const forge_adamw_tensor* tensors, int n_tensors, float lr,
  * The sum is held in fp32 within a thread's few values and in fp64 beyond, and does not
  * overflow or vanish where the norm itself does not.  A NaN among the gradients makes the norm
  * NaN and leaves c = 1; an infinity makes c = 0 (as in forge_adamw_step): callers that want
- * to skip such a step read the norm.  Tensors: fp32, bf16 or fp16, mixed, 16-byte aligned, n
- * contiguous values each; n = 0 is allowed (its pointers may be NULL).  out may be grad (in
- * place); otherwise outputs must not overlap inputs, and no two tensors may overlap.
- * Deterministic (no atomics); the workspace's contents on entry do not matter.
+ * to skip such a step read the norm.  The norm is within 4e-6 of the exact one, c within one
+ * rounding more (it is held in 64 bits where fp32 has no normal number for it).  Tensors: fp32,
+ * bf16 or fp16, mixed, 16-byte aligned, n contiguous values each; n = 0 is allowed (its pointers
+ * may be NULL).  out may be grad (in place); otherwise outputs must not overlap inputs, no two
+ * tensors may overlap, and norm_out and the workspace lie outside them all.  (forge_adamw_step
+ * reads fp32 gradients and clips them by itself: 16-bit ones clipped here are for another
+ * optimizer, or a reduction over ranks.)  Deterministic (no atomics); the workspace's contents on
+ * entry do not matter.
  */
 #define FORGE_GRAD_F32 0
 #define FORGE_GRAD_BF16 1

@@ -287,9 +287,11 @@ size_t forge_qkv_bwd_workspace_size(int d);
  * dq_weight, dk_weight: fp32 [d], required where the weight is given, not overlapping (where q
  * and k share one weight, its gradient is the sum of the two); accumulate = 1 adds to their
  * contents.  The gradients of shared key / value heads are summed in fp32 before
- * anything is rounded.  One launch, and a small second one where a norm weight is given;
- * deterministic (no atomics).  workspace: 16-byte aligned, contents unspecified on entry and
- * on return.  flags: FORGE_ATTN_FP16, FORGE_QKV_ADJACENT, FORGE_QKV_GRAD_F32.
+ * anything is rounded; the weights' are summed in fp32 over a thread's rows (512 at the
+ * largest sizes) and a block's warps, in fp64 beyond.  One launch, and a small second one where a
+ * norm weight is given; deterministic (no atomics).  workspace: 16-byte aligned, contents
+ * unspecified on entry and on return.  flags: FORGE_ATTN_FP16, FORGE_QKV_ADJACENT,
+ * FORGE_QKV_GRAD_F32.
  */
 int forge_qkv_bwd(const forge_qkv_config* config, const void* dq, const void* dk, const void* dv,
                   const forge_qkv_tensor* q, const forge_qkv_tensor* k,
