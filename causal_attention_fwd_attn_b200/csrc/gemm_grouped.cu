@@ -62,7 +62,9 @@ constexpr int kBK = 64;
 constexpr int kHalfM = 128;        // a block's rows of a pair's 256
 constexpr int kAccCols = 256;      // tensor memory columns of one of the two accumulators
 // k-blocks of a reduction's chunk, after which its sums leave tensor memory: for fp32 outputs, and
-// for 16-bit ones (the forward of 16384 rows took 249 us with 8, 242 with 16, 240 with 64).
+// for 16-bit ones (the forward of 16384 rows took 249 us with 8, 242 with 16, 240 with 64).  16-bit
+// outputs of a single chunk are rounded as they leave (LONG = false): by way of the registers of
+// sums 6712 rows of eight experts, 640 -> 992, took 16.0 us instead of 15.3.
 constexpr int kChunk32 = 8, kChunk16 = 64;
 constexpr int kMaxStages = 10;
 constexpr int kMaxSmem = 232448;   // shared memory of a block
@@ -192,9 +194,10 @@ __device__ __forceinline__ void finish(Barriers* bars) {
 // ------------------------------------------------------------------ forward and dX ----
 constexpr int kStageRows = 32;  // token rows of one staging buffer of the epilogue
 
-// BN: tokens of a pair's tile at most.
-template <int BN, bool OUT32>
+// BN: tokens of a pair's tile at most.  LONG: 16-bit outputs whose reduction takes several chunks.
+template <int BN, bool OUT32, bool LONG>
 struct RowsCfg {
+    static constexpr bool kSums = OUT32 || LONG;  // added up in registers
     static constexpr int kABytes = kHalfM * kBK * 2;
     static constexpr int kStageBytes = kABytes + BN / 2 * kBK * 2;
     static constexpr int kRowBytes = kHalfM * (OUT32 ? 4 : 2);
@@ -208,7 +211,7 @@ struct RowsCfg {
         const int fit = (kMaxSmem - kRest - tables_bytes(experts)) / kStageBytes;
         return fit < kMaxStages ? fit : kMaxStages;
     }
-    static_assert(stages(kMaxExperts) >= 4 && kSteps >= 1, "shared memory budget");
+    static_assert(!(OUT32 && LONG) && stages(kMaxExperts) >= 4 && kSteps >= 1, "shared memory budget");
 };
 
 struct RowsShape {
@@ -278,12 +281,12 @@ __device__ __forceinline__ int choose_width(const Tables& t, int experts, int fe
     return BN - 32 * best;
 }
 
-template <int BN, bool W_MN, bool OUT32, bool F16>
+template <int BN, bool W_MN, bool OUT32, bool F16, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ TokenMaps tmap_x,
                         const int* offsets, void* out, const RowsShape s) {
-    using C = RowsCfg<BN, OUT32>;
+    using C = RowsCfg<BN, OUT32, LONG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -349,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const RowsUnit w = rows_unit(tab, most, u, e);
             const uint32_t idesc = kIdesc0 | ((uint32_t)(w.width >> 3) << 17);
             for (int kb0 = 0; ok && kb0 < s.k_blocks; ++n_acc) {
-                const int kb1 = min(kb0 + C::kChunk, s.k_blocks);
+                const int kb1 = C::kSums ? min(kb0 + C::kChunk, s.k_blocks) : s.k_blocks;
                 const int buf = n_acc & 1, use = n_acc >> 1;
                 if (use > 0 &&
                     !warp_wait(&bars->acc_empty[buf], (use - 1) & 1, kSiteAccEmpty, abort)) {
@@ -396,12 +399,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = pair; ok && u < units; u += pairs) {
             const RowsUnit w = rows_unit(tab, most, u, e);
             const int fm = w.fm + (int)rank * kHalfM;
-            float sum[C::kSteps][kStageRows];
+            uint32_t kept[C::kSteps][C::kSums ? 32 : 16];  // sums in fp32, or 16-bit pairs
+            if constexpr (C::kSums) {
 #pragma unroll
-            for (int q = 0; q < C::kSteps; ++q)
+                for (int q = 0; q < C::kSteps; ++q)
 #pragma unroll
-                for (int j = 0; j < kStageRows; ++j) sum[q][j] = 0.f;
-            const int chunks = (s.k_blocks + C::kChunk - 1) / C::kChunk;
+                    for (int j = 0; j < 32; ++j) kept[q][j] = 0u;
+            }
+            const int chunks = C::kSums ? (s.k_blocks + C::kChunk - 1) / C::kChunk : 1;
             for (int c = 0; c < chunks; ++c, ++n_acc) {
                 const int buf = n_acc & 1;
                 // the group goes on, or gives up, together: it meets at barriers below
@@ -415,13 +420,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int c0 = (kGroups * q + (int)group) * kStageRows;
                     if (c0 >= w.width) break;
                     const uint32_t from = tmem + lane_off + buf * kAccCols + c0;
+                    if constexpr (C::kSums) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[16];
-                        tmem_ld16(from + 16 * h, r);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+                            tmem_ld16(from + 16 * h, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                kept[q][16 * h + j] =
+                                    __float_as_uint(__uint_as_float(kept[q][16 * h + j]) +
+                                                    __uint_as_float(r[j]));
+                        }
+                    } else {
+                        uint32_t r[32];
+                        tmem_ld32(from, r);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[q][16 * h + j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 16; ++j)
+                            kept[q][j] = pack16x2<F16>(__uint_as_float(r[2 * j]),
+                                                       __uint_as_float(r[2 * j + 1]));
                     }
                 }
                 tc_fence_before();
@@ -438,10 +456,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kStageRows; j += 2) {
                     uint8_t* dst = staging + j * kRowBytes + (quarter * 32 + lane) * kEl;
                     if constexpr (OUT32) {
-                        *reinterpret_cast<float*>(dst) = sum[q][j];
-                        *reinterpret_cast<float*>(dst + kRowBytes) = sum[q][j + 1];
+                        *reinterpret_cast<uint32_t*>(dst) = kept[q][j];
+                        *reinterpret_cast<uint32_t*>(dst + kRowBytes) = kept[q][j + 1];
                     } else {
-                        const uint32_t two = pack16x2<F16>(sum[q][j], sum[q][j + 1]);
+                        const uint32_t two = LONG ? pack16x2<F16>(__uint_as_float(kept[q][j]),
+                                                                  __uint_as_float(kept[q][j + 1]))
+                                                  : kept[q][j / 2];
                         *reinterpret_cast<uint16_t*>(dst) = (uint16_t)two;
                         *reinterpret_cast<uint16_t*>(dst + kRowBytes) = (uint16_t)(two >> 16);
                     }
@@ -739,12 +759,12 @@ int grid_of(long long units) {
     return 2 * (units < 1 ? 1 : (units < pairs ? (int)units : pairs));
 }
 
-template <int BN, bool W_MN, bool OUT32, bool F16>
+template <int BN, bool W_MN, bool OUT32, bool F16, bool LONG>
 cudaError_t launch_rows_t(const CUtensorMap& tw, const TokenMaps& tx, const int* offsets,
                           void* out, const RowsShape& s, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};
-    auto* kernel = grouped_rows_kernel<BN, W_MN, OUT32, F16>;
-    using C = RowsCfg<BN, OUT32>;
+    auto* kernel = grouped_rows_kernel<BN, W_MN, OUT32, F16, LONG>;
+    using C = RowsCfg<BN, OUT32, LONG>;
     cudaError_t e = set_max_dynamic_smem(kernel, kMaxSmem, configured);
     if (e != cudaSuccess) return e;
     RowsShape shape = s;
@@ -761,10 +781,13 @@ template <int BN, bool W_MN>
 cudaError_t launch_rows_n(const CUtensorMap& tw, const TokenMaps& tx, const int* offsets,
                           void* out, const RowsShape& s, bool f32, bool f16, cudaStream_t cs) {
     if (f32)
-        return f16 ? launch_rows_t<BN, W_MN, true, true>(tw, tx, offsets, out, s, cs)
-                   : launch_rows_t<BN, W_MN, true, false>(tw, tx, offsets, out, s, cs);
-    return f16 ? launch_rows_t<BN, W_MN, false, true>(tw, tx, offsets, out, s, cs)
-               : launch_rows_t<BN, W_MN, false, false>(tw, tx, offsets, out, s, cs);
+        return f16 ? launch_rows_t<BN, W_MN, true, true, false>(tw, tx, offsets, out, s, cs)
+                   : launch_rows_t<BN, W_MN, true, false, false>(tw, tx, offsets, out, s, cs);
+    if (s.k_blocks > kChunk16)
+        return f16 ? launch_rows_t<BN, W_MN, false, true, true>(tw, tx, offsets, out, s, cs)
+                   : launch_rows_t<BN, W_MN, false, false, true>(tw, tx, offsets, out, s, cs);
+    return f16 ? launch_rows_t<BN, W_MN, false, true, false>(tw, tx, offsets, out, s, cs)
+               : launch_rows_t<BN, W_MN, false, false, false>(tw, tx, offsets, out, s, cs);
 }
 
 template <bool W_MN>
